@@ -69,7 +69,9 @@ typedef enum {
     LCI_ERR_TIMEOUT = 6        /* a bounded device wait gave up (sticky word) */
 } lci_status;
 
-typedef enum { LCI_F32 = 0, LCI_BF16 = 1 } lci_dtype;
+/* LCI_E4M3 (8-bit floats, 4 exponent and 3 mantissa bits, no infinities) is a
+ * type of KV pools only: the pools of the q8 entry points below. */
+typedef enum { LCI_F32 = 0, LCI_BF16 = 1, LCI_E4M3 = 2 } lci_dtype;
 
 /* Which kernel family runs. AUTO: DECODE when S == 1, PREFILL otherwise.
  * Both produce identical block ids for identical inputs ([GPU-stack],
@@ -100,6 +102,10 @@ LCI_API const char* lci_last_error(void);
  *   block_size   tokens per page.
  *   num_kv_heads, head_dim, kv_dtype: shape and type of the pools
  *                K, V = [num_pages][num_kv_heads][block_size][head_dim].
+ *                A table with LCI_E4M3 pools serves the q8 entry points and
+ *                everything that reads no pool (paged block keys, index
+ *                selection, eviction); the other attention entry points
+ *                refuse it (LCI_ERR_UNSUPPORTED).
  * Allocates only the host object. Returns LCI_ERR_INVALID_ARG on a null
  * pointer or a non-positive size.
  */
@@ -329,6 +335,147 @@ LCI_API lci_status lci_sparse_attn_partial(const void* q, int32_t batch, int32_t
 LCI_API lci_status lci_attn_merge(const void* d_o, const float* d_lse, lci_dtype dtype,
                                   int32_t nlists, int64_t rows_heads, int32_t head_dim,
                                   void* d_out, void* stream);
+
+/*
+ * The 8-bit paged KV cache. Pools of e4m3 codes with one fp32 scale per page
+ * and KV head:
+ *   k_pool, v_pool    [num_pages][num_kv_heads][block_size][head_dim], 1 byte
+ *                     per element, 16-byte aligned
+ *   k_scale, v_scale  [num_pages][num_kv_heads] float
+ * A stored element stands for scale * value(code). The table is created with
+ * LCI_E4M3. Half the bytes of a bf16 cache: twice the context per GPU, and a
+ * decode step reads half as much.
+ */
+
+/*
+ * Append: new tokens' K and V enter the cache.
+ *   k_new, v_new [batch][T][num_kv_heads][head_dim], device, dtype (fp32 or
+ *                bf16)
+ *   d_start  [batch] int32: position of a sequence's first new token (>= 0);
+ *            positions below it in its block are already stored
+ *   d_count  [batch] int32 or NULL: new tokens of each sequence, clamped to
+ *            0 .. T (NULL: T for all); the rest of the row is not read
+ * For every touched page and KV head, and K and V apart:
+ *   need   = the smallest 2^e, e >= -60, with |x| <= 448 * 2^e for every
+ *            finite new element x
+ *   scale' = max(scale, need) if the page already holds tokens of the block,
+ *            else need
+ *   stored codes become e4m3(value * scale / scale'), new ones
+ *            e4m3(x / scale'), to nearest even, saturating at +-448; NaN is
+ *            kept.
+ * Slots behind the last token are left as they were. T = 1 is the decode step.
+ * The touched pages of the call must be distinct (no page shared between its
+ * sequences). A block index >= max_blocks, a negative start or a page outside
+ * [0, num_pages) skips that part and sets the device status word.
+ */
+LCI_API lci_status lci_kv_append_q8(const void* k_new, const void* v_new, lci_dtype dtype,
+                                    int32_t batch, int32_t T, const int32_t* d_start,
+                                    const int32_t* d_count, const lci_block_table* table,
+                                    void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+                                    void* stream);
+
+/*
+ * Changes of the scores before the softmax; zero-initialise, then set what is
+ * wanted. With z the scaled logit of query position p and token t:
+ *   cap > 0      z becomes cap * tanh(z / cap)
+ *   d_slopes     [H_q] float: slopes[h] * |p - t| is subtracted (after the cap)
+ *   d_first      [batch][S] int32: tokens before d_first[b][s] are not attended
+ *                (a document mask: the start of the query's document)
+ *   d_last       [batch][S] int32: replaces p as the last attendable token (a
+ *                prefix mask: max(p, prefix - 1)); ctx_len - 1 still bounds it
+ */
+typedef struct {
+    float cap;
+    const float* d_slopes;
+    const int32_t* d_first;
+    const int32_t* d_last;
+} lci_score_options;
+
+/*
+ * lci_sparse_attn over the 8-bit cache: the same q, ids, positions, masking and
+ * results, with K_t and V_t the values the codes stand for.
+ *   q        [batch][S][H_q][head_dim], device, dtype (fp32 or bf16), 16-byte
+ *            aligned
+ *   k_scale, v_scale  positive and finite; a v_scale below 2^-60 counts as
+ *            2^-60
+ *   options  NULL, or the score changes above
+ *   out      [batch][S][H_q][head_dim], device, dtype, 16-byte aligned (output)
+ *   d_lse    [batch][S][H_q] float or NULL (output): log2 of the sum of
+ *            2^(log2(e) * z) over the attended tokens, -inf where there are none
+ *   d_mass   [batch][S][num_kv_heads][topk] float or NULL (output): the softmax
+ *            weight that the tokens of block d_ids[b][s][i] received, summed
+ *            over the query heads of the KV head; 0 for -1 entries. A row's
+ *            entries add up to H_q / num_kv_heads (0 where nothing is attended).
+ * A row without an attended token is zero. Rows of d_ids may be in any order,
+ * may hold -1 anywhere, and must not repeat a block. Slots that are not
+ * attended are never read into a result, whatever they hold. Softmax, sums and
+ * accumulation are fp32; on the tensor cores (bf16 q, head_dim 128, block_size
+ * a multiple of 64, at most 16 query heads per KV head) codes are multiplied
+ * exactly and softmax weights are rounded to 11 bits (row-wise schedule) or 8
+ * bits (tile schedule). LCI_PHASE_PREFILL asks for the tile schedule, DECODE for
+ * the row-wise one, AUTO chooses by the sizes; a call with d_mass takes the
+ * row-wise one.
+ * Limits: H_q a multiple of num_kv_heads, head_dim a multiple of 32 and <= 256,
+ * topk <= 256, max_blocks * block_size < 2^31. Needs no workspace.
+ */
+LCI_API lci_status lci_sparse_attn_q8(const void* q, lci_dtype dtype, int32_t batch, int32_t S,
+                                      int32_t H_q, const void* k_pool, const void* v_pool,
+                                      const float* k_scale, const float* v_scale,
+                                      const lci_block_table* table, const int32_t* d_ids,
+                                      int32_t topk, const int32_t* d_ctx_len,
+                                      const int32_t* d_q_start, float scale,
+                                      const lci_score_options* options, lci_phase phase, void* out,
+                                      float* d_lse, float* d_mass, void* stream);
+
+/*
+ * Accumulates the attention weight that blocks received:
+ *   d_weight[b][j] = decay * d_weight[b][j]
+ *                    + sum over s, i with d_ids[b][s][i] == j, and over g, of
+ *                      d_mass[b][s][g][i]
+ *   d_ids    [batch][S][topk] int32, -1 padded, a row's ids distinct
+ *   d_mass   [batch][S][num_kv_heads][topk] float (lci_sparse_attn_q8's)
+ *   d_weight [batch][max_blocks] float (updated in place)
+ *   decay    finite and >= 0 (1: a plain sum; below 1 the past fades)
+ * Sums run in a fixed order: the same inputs give the same bits. An id outside
+ * [-1, max_blocks) is skipped and sets the device status word.
+ * Limits: max_blocks <= 16384, topk <= 256.
+ */
+LCI_API lci_status lci_block_weight_update(const int32_t* d_ids, const float* d_mass,
+                                           int32_t batch, int32_t S, int32_t num_kv_heads,
+                                           int32_t topk, int32_t max_blocks, float decay,
+                                           float* d_weight, void* stream);
+
+/*
+ * Eviction: every sequence of more than `budget` blocks keeps its first `sink`
+ * blocks, its last `recent` ones (the partly filled last block among them) and,
+ * of the rest, the budget - sink - recent with the largest weight (ties to the
+ * lower block id; NaN counts as the largest).
+ *   table      the block table; any pool type
+ *   d_ctx_len  [batch] int32, d_weight [batch][max_blocks] float
+ *   d_table_out  [batch][max_blocks] int32: the row's kept pages in block
+ *              order, then the freed pages in block order, then the entries
+ *              past the sequence's blocks unchanged. The freed pages follow the
+ *              kept ones directly: the sequence can grow into them, or the
+ *              caller takes d_freed[b] pages from there.
+ *   d_ctx_out  [batch] int32: d_ctx_len - block_size * freed blocks
+ *   d_weight_out [batch][max_blocks] float: weights of the kept blocks in the
+ *              new order, 0 behind them
+ *   d_kept     [batch][budget] int32 or NULL: old ids of the kept blocks,
+ *              ascending, -1 padded
+ *   d_freed    [batch] int32 or NULL: number of freed blocks
+ * Outputs may be the inputs (the table's own memory, d_ctx_len, d_weight): the
+ * update is then in place. Kept tokens move up in position, in order; whatever
+ * is stored per page (K, V, scales, paged block keys) stays valid, what is
+ * stored per block of a sequence (a dense k_c) does not. A sequence with
+ * ctx_len > max_blocks * block_size is left as it is and sets the device status
+ * word.
+ * Limits: 1 <= recent, 0 <= sink, sink + recent <= budget, max_blocks <= 16384.
+ */
+LCI_API lci_status lci_cache_evict(const lci_block_table* table, int32_t batch,
+                                   const int32_t* d_ctx_len, const float* d_weight, int32_t budget,
+                                   int32_t sink, int32_t recent, int32_t* d_table_out,
+                                   int32_t* d_ctx_out, float* d_weight_out, int32_t* d_kept,
+                                   int32_t* d_freed, void* stream);
 
 /*
  * lci_index_select without any device allocation. The reference pages have no

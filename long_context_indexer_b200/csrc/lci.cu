@@ -17,13 +17,16 @@
 #include "../../include/lci.h"
 #include "attn_decode.cuh"
 #include "attn_prefill.cuh"
+#include "attn_q8_simt.cuh"
 #include "attn_simt.cuh"
+#include "cache_evict.cuh"
 #include "common.cuh"
 #include "compress.cuh"
 #include "cp_merge.cuh"
 #include "decode_fused.cuh"
 #include "index_gemv.cuh"
 #include "index_prefill.cuh"
+#include "q8_cache.cuh"
 #include "state_scan.cuh"
 #include "topk_select.cuh"
 
@@ -262,6 +265,9 @@ lci_status launch_index_gemv(const void* q_c, const void* k_c, int32_t batch, in
 lci_status check_attn_args(int32_t batch, int32_t S, int32_t H_q, const lci_block_table* t,
                            int32_t topk) {
     if (!t) return fail(LCI_ERR_INVALID_ARG, "sparse_attn: null block table");
+    if (t->dtype == LCI_E4M3)
+        return fail(LCI_ERR_UNSUPPORTED, "sparse_attn: the block table's pools are e4m3 "
+                    "(lci_sparse_attn_q8)");
     if (batch <= 0 || S <= 0 || H_q <= 0 || topk <= 0)
         return fail(LCI_ERR_INVALID_ARG, "sparse_attn: sizes must be positive (batch=%d S=%d H_q=%d "
                     "topk=%d)", batch, S, H_q, topk);
@@ -633,7 +639,8 @@ lci_status lci_create_block_table(const int32_t* d_table, int32_t batch, int32_t
     if (batch <= 0 || max_blocks <= 0 || num_pages <= 0 || block_size <= 0 || num_kv_heads <= 0 ||
         head_dim <= 0)
         return fail(LCI_ERR_INVALID_ARG, "create_block_table: sizes must be positive");
-    if (!dtype_ok(kv_dtype)) return fail(LCI_ERR_INVALID_ARG, "create_block_table: unknown dtype");
+    if (!dtype_ok(kv_dtype) && kv_dtype != LCI_E4M3)
+        return fail(LCI_ERR_INVALID_ARG, "create_block_table: unknown dtype");
     lci_block_table* t = new (std::nothrow) lci_block_table;
     if (!t) return fail(LCI_ERR_INVALID_ARG, "create_block_table: host allocation failed");
     t->d_table = d_table;
@@ -1391,6 +1398,225 @@ lci_status lci_sparse_attn_pipelined(const void* q, int32_t batch, int32_t S, in
     return launch_attn_decode(q, batch, S, H_q, k_pool, v_pool, table, d_ids, topk, d_ctx_len,
                               d_q_start, scale, out, static_cast<cudaStream_t>(stream),
                               reinterpret_cast<const unsigned int*>(d_ready), false);
+}
+
+}  // extern "C"
+
+// ---- the 8-bit paged cache: append, attention, block weights, eviction ----
+
+namespace {
+
+lci_status check_q8_table(const char* what, const lci_block_table* t, int32_t batch) {
+    if (!t) return fail(LCI_ERR_INVALID_ARG, "%s: null block table", what);
+    if (t->dtype != LCI_E4M3)
+        return fail(LCI_ERR_INVALID_ARG, "%s: the block table's pools are not e4m3", what);
+    if (batch <= 0 || batch > t->batch)
+        return fail(LCI_ERR_INVALID_ARG, "%s: batch %d outside 1 .. %d (the table's)", what, batch,
+                    t->batch);
+    return LCI_OK;
+}
+
+template <typename T, int VEC>
+void launch_kv_append(const void* k_new, const void* v_new, int32_t batch, int32_t T_new,
+                      const int32_t* start, const int32_t* count, const lci_block_table* t,
+                      void* k_pool, void* v_pool, float* k_scale, float* v_scale, int slots,
+                      cudaStream_t st) {
+    const dim3 grid((unsigned)((long long)batch * slots * t->num_kv_heads), 2);
+    lci::kv_append_q8_kernel<T, VEC><<<grid, 256, 0, st>>>(
+        static_cast<const T*>(k_new), static_cast<const T*>(v_new), batch, T_new, t->num_kv_heads,
+        t->head_dim, t->block_size, start, count, t->d_table, t->max_blocks, t->num_pages, slots,
+        static_cast<uint8_t*>(k_pool), static_cast<uint8_t*>(v_pool), k_scale, v_scale);
+}
+
+template <typename T>
+lci_status launch_attn_q8_simt(const lci::AttnQ8Args& a, int32_t batch, cudaStream_t st) {
+    const size_t smem = (size_t)(a.hd * (1 + lci::kQ8SimtWarps) + 2 * lci::kQ8SimtWarps +
+                                 3 * a.topk) * 4;
+    const dim3 grid((unsigned)(batch * a.S), (unsigned)a.H_kv);
+    lci::sparse_attn_q8_simt_kernel<T><<<grid, lci::kQ8SimtWarps * 32, smem, st>>>(a);
+    return check_launch("sparse_attn_q8");
+}
+
+template <int IPT>
+void launch_evict(const lci_block_table* t, int32_t batch, const int32_t* ctx_len,
+                  const float* weight, int32_t budget, int32_t sink, int32_t recent,
+                  int32_t* table_out, int32_t* ctx_out, float* weight_out, int32_t* kept,
+                  int32_t* freed, cudaStream_t st) {
+    const int threads = ((t->max_blocks + IPT - 1) / IPT + 31) / 32 * 32;
+    lci::cache_evict_kernel<IPT><<<(unsigned)batch, threads, 0, st>>>(
+        t->d_table, ctx_len, weight, t->max_blocks, t->block_size, budget, sink, recent, table_out,
+        ctx_out, weight_out, kept, freed);
+}
+
+}  // namespace
+
+extern "C" {
+
+lci_status lci_kv_append_q8(const void* k_new, const void* v_new, lci_dtype dtype, int32_t batch,
+                            int32_t T, const int32_t* d_start, const int32_t* d_count,
+                            const lci_block_table* table, void* k_pool, void* v_pool,
+                            float* k_scale, float* v_scale, void* stream) {
+    if (!k_new || !v_new || !d_start || !k_pool || !v_pool || !k_scale || !v_scale)
+        return fail(LCI_ERR_INVALID_ARG, "kv_append_q8: null pointer argument");
+    lci_status st = check_q8_table("kv_append_q8", table, batch);
+    if (st != LCI_OK) return st;
+    if (T <= 0) return fail(LCI_ERR_INVALID_ARG, "kv_append_q8: T must be positive");
+    if (!dtype_ok(dtype))
+        return fail(LCI_ERR_INVALID_ARG, "kv_append_q8: unknown dtype %d", (int)dtype);
+    if (!aligned16(k_pool) || !aligned16(v_pool))
+        return fail(LCI_ERR_INVALID_ARG, "kv_append_q8: pools must be 16-byte aligned");
+    const int slots = (int)(((long long)T - 1 + table->block_size - 1) / table->block_size + 1);
+    const long long ctas = (long long)batch * slots * table->num_kv_heads;
+    if (ctas >= (1ll << 31) || (long long)table->block_size * table->head_dim >= (1ll << 31))
+        return fail(LCI_ERR_UNSUPPORTED, "kv_append_q8: sizes too large");
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    // 16 elements per access where rows allow it, else one
+    const bool vec = table->head_dim % 16 == 0 && aligned16(k_new) && aligned16(v_new);
+    auto run = dtype == LCI_F32 ? (vec ? launch_kv_append<float, 16> : launch_kv_append<float, 1>)
+                                : (vec ? launch_kv_append<__nv_bfloat16, 16>
+                                       : launch_kv_append<__nv_bfloat16, 1>);
+    run(k_new, v_new, batch, T, d_start, d_count, table, k_pool, v_pool, k_scale, v_scale, slots, cs);
+    return check_launch("kv_append_q8");
+}
+
+lci_status lci_sparse_attn_q8(const void* q, lci_dtype dtype, int32_t batch, int32_t S, int32_t H_q,
+                              const void* k_pool, const void* v_pool, const float* k_scale,
+                              const float* v_scale, const lci_block_table* table,
+                              const int32_t* d_ids, int32_t topk, const int32_t* d_ctx_len,
+                              const int32_t* d_q_start, float scale,
+                              const lci_score_options* options, lci_phase phase, void* out,
+                              float* d_lse, float* d_mass, void* stream) {
+    if (!q || !k_pool || !v_pool || !k_scale || !v_scale || !d_ids || !d_ctx_len || !d_q_start ||
+        !out)
+        return fail(LCI_ERR_INVALID_ARG, "sparse_attn_q8: null pointer argument");
+    lci_status st = check_q8_table("sparse_attn_q8", table, batch);
+    if (st != LCI_OK) return st;
+    if (S <= 0 || H_q <= 0 || topk <= 0)
+        return fail(LCI_ERR_INVALID_ARG, "sparse_attn_q8: sizes must be positive (S=%d H_q=%d "
+                    "topk=%d)", S, H_q, topk);
+    if (!dtype_ok(dtype))
+        return fail(LCI_ERR_INVALID_ARG, "sparse_attn_q8: unknown dtype %d", (int)dtype);
+    if (phase != LCI_PHASE_AUTO && phase != LCI_PHASE_PREFILL && phase != LCI_PHASE_DECODE)
+        return fail(LCI_ERR_INVALID_ARG, "sparse_attn_q8: unknown phase %d", (int)phase);
+    if (H_q % table->num_kv_heads != 0)
+        return fail(LCI_ERR_INVALID_ARG, "sparse_attn_q8: H_q %d not a multiple of num_kv_heads %d",
+                    H_q, table->num_kv_heads);
+    if (!aligned16(q) || !aligned16(out) || !aligned16(k_pool) || !aligned16(v_pool))
+        return fail(LCI_ERR_INVALID_ARG, "sparse_attn_q8: q, out and the pools must be 16-byte "
+                    "aligned");
+    if (!(scale > 0.f)) scale = 1.0f / std::sqrt((float)table->head_dim);
+    if (!std::isfinite(scale))
+        return fail(LCI_ERR_INVALID_ARG, "sparse_attn_q8: non-finite scale");
+    lci_score_options opt = {};
+    if (options) opt = *options;
+    if (!std::isfinite(opt.cap) || opt.cap < 0.f)
+        return fail(LCI_ERR_INVALID_ARG, "sparse_attn_q8: cap must be finite and >= 0");
+    if (topk > lci::kMaxTopk)
+        return fail(LCI_ERR_UNSUPPORTED, "sparse_attn_q8: topk %d above %d", topk, lci::kMaxTopk);
+    if (table->head_dim % 32 != 0 || table->head_dim > lci::kQ8MaxHd)
+        return fail(LCI_ERR_UNSUPPORTED, "sparse_attn_q8: head_dim %d must be a multiple of 32 and "
+                    "<= %d", table->head_dim, lci::kQ8MaxHd);
+    if ((long long)table->max_blocks * table->block_size >= (1ll << 31) ||
+        (long long)batch * S >= (1ll << 31) || table->num_kv_heads > 65535)
+        return fail(LCI_ERR_UNSUPPORTED, "sparse_attn_q8: sizes too large");
+    lci::AttnQ8Args a = {};
+    a.q = q;
+    a.k = static_cast<const uint8_t*>(k_pool);
+    a.v = static_cast<const uint8_t*>(v_pool);
+    a.ks = k_scale;
+    a.vs = v_scale;
+    a.table = table->d_table;
+    a.nb_max = table->max_blocks;
+    a.num_pages = table->num_pages;
+    a.H_kv = table->num_kv_heads;
+    a.bs = table->block_size;
+    a.hd = table->head_dim;
+    a.S = S;
+    a.H_q = H_q;
+    a.ids = d_ids;
+    a.topk = topk;
+    a.ctx_len = d_ctx_len;
+    a.q_start = d_q_start;
+    a.scale = scale;
+    a.cap = opt.cap;
+    a.slopes = opt.d_slopes;
+    a.first = opt.d_first;
+    a.last = opt.d_last;
+    a.out = out;
+    a.lse = d_lse;
+    a.mass = d_mass;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    return dtype == LCI_F32 ? launch_attn_q8_simt<float>(a, batch, cs)
+                            : launch_attn_q8_simt<__nv_bfloat16>(a, batch, cs);
+}
+
+lci_status lci_block_weight_update(const int32_t* d_ids, const float* d_mass, int32_t batch,
+                                   int32_t S, int32_t num_kv_heads, int32_t topk,
+                                   int32_t max_blocks, float decay, float* d_weight, void* stream) {
+    if (!d_ids || !d_mass || !d_weight)
+        return fail(LCI_ERR_INVALID_ARG, "block_weight_update: null pointer argument");
+    if (batch <= 0 || S <= 0 || num_kv_heads <= 0 || topk <= 0 || max_blocks <= 0)
+        return fail(LCI_ERR_INVALID_ARG, "block_weight_update: sizes must be positive");
+    if (!std::isfinite(decay) || decay < 0.f)
+        return fail(LCI_ERR_INVALID_ARG, "block_weight_update: decay must be finite and >= 0");
+    if (topk > lci::kMaxTopk || max_blocks > kMaxNbMax || batch > 65535)
+        return fail(LCI_ERR_UNSUPPORTED, "block_weight_update: topk above %d, max_blocks above %d or "
+                    "batch above 65535", lci::kMaxTopk, kMaxNbMax);
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [] {
+        attr_err = cudaFuncSetAttribute(lci::block_weight_update_kernel,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)lci::bwu::smem_bytes(lci::bwu::kMaxWarps));
+    });
+    if (attr_err != cudaSuccess)
+        return fail(LCI_ERR_CUDA, "block_weight_update: %s", cudaGetErrorString(attr_err));
+    // a few rows per warp: up to 16 warps, then up to 8 CTAs
+    const int ranges = (max_blocks + lci::bwu::kRange - 1) / lci::bwu::kRange;
+    int nsplit = 1;
+    while (nsplit < lci::bwu::kMaxSplit &&
+           S > nsplit * lci::bwu::kMaxWarps * lci::bwu::kRowsAhead) nsplit *= 2;
+    int warps = 4;
+    while (warps < lci::bwu::kMaxWarps && S > nsplit * warps * lci::bwu::kRowsAhead) warps *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)nsplit, (unsigned)ranges, (unsigned)batch);
+    cfg.blockDim = dim3((unsigned)warps * 32);
+    cfg.dynamicSmemBytes = lci::bwu::smem_bytes(warps);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)nsplit;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = nsplit > 1 ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, lci::block_weight_update_kernel, d_ids, d_mass, S,
+                                             num_kv_heads, topk, max_blocks, decay, d_weight, nsplit);
+    if (e != cudaSuccess) return fail(LCI_ERR_CUDA, "block_weight_update: %s", cudaGetErrorString(e));
+    return check_launch("block_weight_update");
+}
+
+lci_status lci_cache_evict(const lci_block_table* table, int32_t batch, const int32_t* d_ctx_len,
+                           const float* d_weight, int32_t budget, int32_t sink, int32_t recent,
+                           int32_t* d_table_out, int32_t* d_ctx_out, float* d_weight_out,
+                           int32_t* d_kept, int32_t* d_freed, void* stream) {
+    if (!table || !d_ctx_len || !d_weight || !d_table_out || !d_ctx_out || !d_weight_out)
+        return fail(LCI_ERR_INVALID_ARG, "cache_evict: null pointer argument");
+    if (batch <= 0 || batch > table->batch)
+        return fail(LCI_ERR_INVALID_ARG, "cache_evict: batch %d outside 1 .. %d (the table's)",
+                    batch, table->batch);
+    if (sink < 0 || recent < 1 || budget < 1 || (long long)sink + recent > budget)
+        return fail(LCI_ERR_INVALID_ARG, "cache_evict: needs sink >= 0, recent >= 1 and sink + "
+                    "recent <= budget (sink=%d recent=%d budget=%d)", sink, recent, budget);
+    if (table->max_blocks > kMaxNbMax)
+        return fail(LCI_ERR_UNSUPPORTED, "cache_evict: max_blocks %d above %d", table->max_blocks,
+                    kMaxNbMax);
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    // blocks per thread: up to 1024 threads
+    const int nb = table->max_blocks;
+    auto run = nb <= 1024 ? launch_evict<1> : nb <= 4096 ? launch_evict<4> : launch_evict<16>;
+    run(table, batch, d_ctx_len, d_weight, budget, sink, recent, d_table_out, d_ctx_out,
+        d_weight_out, d_kept, d_freed, cs);
+    return check_launch("cache_evict");
 }
 
 }  // extern "C"

@@ -23,7 +23,7 @@ LCI_OK = 0
 STATUS_NAMES = {0: "LCI_OK", 1: "LCI_ERR_INVALID_ARG", 2: "LCI_ERR_UNSUPPORTED",
                 3: "LCI_ERR_WORKSPACE", 4: "LCI_ERR_CUDA", 5: "LCI_ERR_DEVICE_BOUNDS",
                 6: "LCI_ERR_TIMEOUT"}
-LCI_F32, LCI_BF16 = 0, 1
+LCI_F32, LCI_BF16, LCI_E4M3 = 0, 1, 2
 PHASES = {"auto": 0, "prefill": 1, "decode": 2}
 
 # Every entry point of include/lci.h: name -> (restype, argtypes)
@@ -73,6 +73,11 @@ SIGNATURES = {
                                                     ctypes.POINTER(_sz)]),
     "lci_index_select_paged": (_st, [_vp, _vp, _st, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i32,
                                      _st, _vp, _vp, _sz, _vp]),
+    "lci_kv_append_q8": (_st, [_vp, _vp, _st, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "lci_sparse_attn_q8": (_st, [_vp, _st, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
+                                 _vp, _vp, _f32, _vp, _st, _vp, _vp, _vp, _vp]),
+    "lci_block_weight_update": (_st, [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp]),
+    "lci_cache_evict": (_st, [_vp, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
     "lci_get_wait_limit_ns": (_st, [ctypes.POINTER(ctypes.c_uint64)]),
 }
 
@@ -178,9 +183,9 @@ class BlockTable:
         self.dtype = dtype
         handle = ctypes.c_void_p()
         lib = load_library()
+        code = LCI_E4M3 if dtype == torch.float8_e4m3fn else _dtype_code(torch.empty(0, dtype=dtype))
         _check(lib.lci_create_block_table(ptr, self.batch, self.max_blocks, self.num_pages,
-                                          self.block_size, self.num_kv_heads, self.head_dim,
-                                          _dtype_code(torch.empty(0, dtype=dtype)),
+                                          self.block_size, self.num_kv_heads, self.head_dim, code,
                                           ctypes.byref(handle)), "lci_create_block_table")
         self._handle = handle
         self._lib = lib
@@ -521,6 +526,237 @@ def gated_state_scan(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gate: to
         _dev(state_out, "state_out", torch.float32, 4), B, T, H, dk, dv, chunk,
         _dev(out, "out", torch.float32, 4), _stream(stream)), "lci_gated_state_scan")
     return out, state_out
+
+
+# ---------------------------------------------------------------- 8-bit paged cache
+
+class _ScoreOptions(ctypes.Structure):
+    _fields_ = [("cap", _f32), ("d_slopes", _vp), ("d_first", _vp), ("d_last", _vp)]
+
+
+class PreparedCall:
+    """A checked call of one entry point, for a loop that makes it every step:
+    the tensors were checked and their pointers taken when it was prepared, and
+    each call launches it on the current stream of the tensors' device, or on
+    ``stream``. It works on the same tensors every time; ``result`` holds the
+    outputs. Returns ``result``."""
+
+    def __init__(self, name: str, args: tuple, result, device: torch.device, keep: tuple):
+        self.result = result
+        self._name, self._args, self._keep = name, args, keep
+        self._fn = getattr(load_library(), name)
+        self._device = device.index
+
+    def __call__(self, stream=None):
+        raw = (torch.cuda.current_stream(self._device) if stream is None else stream).cuda_stream
+        if torch.cuda.current_device() == self._device:
+            rc = self._fn(*self._args, raw)
+        else:
+            with torch.cuda.device(self._device):
+                rc = self._fn(*self._args, raw)
+        if rc != LCI_OK:
+            _check(rc, self._name)
+        return self.result
+
+
+def _opt(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape: tuple):
+    """Pointer of an optional tensor of a given type and shape (NULL if absent)."""
+    return None if t is None else _shaped(t, name, dtype, shape)
+
+
+def _shaped(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple):
+    p = _dev(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"lci: {name} must be {list(shape)}, got {list(t.shape)}")
+    return p
+
+
+def _one_device(*tensors) -> torch.device:
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError(f"lci: tensors are on different devices: {sorted(map(str, devices))}")
+    return devices.pop()
+
+
+class Q8Cache:
+    """A paged KV cache held in 8 bits: e4m3 pools ``k``, ``v`` [num_pages, H_kv,
+    block_size, head_dim] and a scale per page and KV head, ``k_scale``,
+    ``v_scale`` [num_pages, H_kv] fp32. An element stands for scale * value."""
+
+    def __init__(self, num_pages: int, num_kv_heads: int, block_size: int, head_dim: int, device):
+        shape = (num_pages, num_kv_heads, block_size, head_dim)
+        self.k = torch.zeros(shape, dtype=torch.float8_e4m3fn, device=device)
+        self.v = torch.zeros(shape, dtype=torch.float8_e4m3fn, device=device)
+        self.k_scale = torch.ones(shape[:2], dtype=torch.float32, device=device)
+        self.v_scale = torch.ones(shape[:2], dtype=torch.float32, device=device)
+
+    @classmethod
+    def wrap(cls, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
+             v_scale: torch.Tensor) -> "Q8Cache":
+        """A cache over existing tensors."""
+        c = cls.__new__(cls)
+        c.k, c.v, c.k_scale, c.v_scale = k, v, k_scale, v_scale
+        return c
+
+    def _pointers(self, table: "BlockTable"):
+        shape = (table.num_pages, table.num_kv_heads, table.block_size, table.head_dim)
+        if table.dtype != torch.float8_e4m3fn:
+            raise TypeError("lci: the block table is not over e4m3 pools")
+        return (_shaped(self.k, "k pool", torch.float8_e4m3fn, shape),
+                _shaped(self.v, "v pool", torch.float8_e4m3fn, shape),
+                _shaped(self.k_scale, "k_scale", torch.float32, shape[:2]),
+                _shaped(self.v_scale, "v_scale", torch.float32, shape[:2]))
+
+    def append(self, k_new: torch.Tensor, v_new: torch.Tensor, start: torch.Tensor,
+               table: "BlockTable", count: Optional[torch.Tensor] = None, stream=None) -> None:
+        """Append k_new, v_new [B, T, H_kv, hd] at positions start[b] ..; see kv_append_q8."""
+        kv_append_q8(self, table, k_new, v_new, start, count=count, stream=stream)
+
+
+def prepare_kv_append_q8(cache: Q8Cache, table: BlockTable, k_new: torch.Tensor,
+                         v_new: torch.Tensor, start: torch.Tensor,
+                         count: Optional[torch.Tensor] = None) -> PreparedCall:
+    """kv_append_q8 as a PreparedCall."""
+    B, T = k_new.shape[:2]
+    shape = (B, T, table.num_kv_heads, table.head_dim)
+    kp, vp, ks, vs = cache._pointers(table)
+    dev = _one_device(table.table, cache.k, cache.v, cache.k_scale, cache.v_scale, k_new, v_new,
+                      start, count)
+    args = (_shaped(k_new, "k_new", k_new.dtype, shape), _shaped(v_new, "v_new", k_new.dtype, shape),
+            _dtype_code(k_new), B, T, _shaped(start, "start", torch.int32, (B,)),
+            _opt(count, "count", torch.int32, (B,)), table.handle, kp, vp, ks, vs)
+    return PreparedCall("lci_kv_append_q8", args, (cache.k, cache.v, cache.k_scale, cache.v_scale),
+                        dev, (cache, table, k_new, v_new, start, count))
+
+
+def kv_append_q8(cache: Q8Cache, table: BlockTable, k_new: torch.Tensor, v_new: torch.Tensor,
+                 start: torch.Tensor, count: Optional[torch.Tensor] = None, stream=None):
+    """New tokens' K and V [B, T, H_kv, hd] (bf16 or fp32) enter the cache at
+    positions start[b] .. (count[b] of them, T where count is None). A page's
+    scale grows when a new token needs it; stored codes are then rounded to it.
+    Returns (k, v, k_scale, v_scale), the cache's own tensors."""
+    return prepare_kv_append_q8(cache, table, k_new, v_new, start, count)(stream)
+
+
+def prepare_sparse_attn_q8(q: torch.Tensor, cache: Q8Cache, table: BlockTable, ids: torch.Tensor,
+                           ctx_len: torch.Tensor, q_start: torch.Tensor, scale: float = 0.0,
+                           cap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+                           first: Optional[torch.Tensor] = None,
+                           last: Optional[torch.Tensor] = None, phase: str = "auto",
+                           out: Optional[torch.Tensor] = None, lse=False,
+                           mass=False) -> PreparedCall:
+    """sparse_attn_q8 as a PreparedCall."""
+    if q.dim() != 4 or ids.dim() != 3:
+        raise ValueError("lci: q must be [B, S, H_q, hd] and ids [B, S, topk]")
+    B, S, H_q, hd = q.shape
+    topk = ids.shape[-1]
+    if hd != table.head_dim:
+        raise ValueError("lci: q's head_dim differs from the block table's")
+    kp, vp, ks, vs = cache._pointers(table)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is True:
+        lse = torch.empty((B, S, H_q), dtype=torch.float32, device=q.device)
+    if mass is True:
+        mass = torch.empty((B, S, table.num_kv_heads, topk), dtype=torch.float32, device=q.device)
+    lse = None if lse is False else lse
+    mass = None if mass is False else mass
+    dev = _one_device(q, table.table, cache.k, cache.v, cache.k_scale, cache.v_scale, ids, ctx_len,
+                      q_start, slopes, first, last, out, lse, mass)
+    options = _ScoreOptions(float(cap), _opt(slopes, "slopes", torch.float32, (H_q,)),
+                            _opt(first, "first", torch.int32, (B, S)),
+                            _opt(last, "last", torch.int32, (B, S)))
+    args = (_dev(q, "q", None, 4), _dtype_code(q), B, S, H_q, kp, vp, ks, vs, table.handle,
+            _shaped(ids, "ids", torch.int32, (B, S, topk)), topk,
+            _shaped(ctx_len, "ctx_len", torch.int32, (B,)),
+            _shaped(q_start, "q_start", torch.int32, (B,)), float(scale), ctypes.byref(options),
+            PHASES[phase], _shaped(out, "out", q.dtype, tuple(q.shape)),
+            _opt(lse, "lse", torch.float32, (B, S, H_q)),
+            _opt(mass, "mass", torch.float32, (B, S, table.num_kv_heads, topk)))
+    result = out if lse is None and mass is None else tuple(
+        t for t in (out, lse, mass) if t is not None)
+    return PreparedCall("lci_sparse_attn_q8", args, result, dev,
+                        (q, cache, table, ids, ctx_len, q_start, slopes, first, last, options, out,
+                         lse, mass))
+
+
+def sparse_attn_q8(q: torch.Tensor, cache: Q8Cache, table: BlockTable, ids: torch.Tensor,
+                   ctx_len: torch.Tensor, q_start: torch.Tensor, scale: float = 0.0,
+                   cap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+                   first: Optional[torch.Tensor] = None, last: Optional[torch.Tensor] = None,
+                   phase: str = "auto", out: Optional[torch.Tensor] = None, lse=False, mass=False,
+                   stream=None):
+    """A3+A4 over the 8-bit cache: attention of q [B, S, H_q, hd] (bf16 or fp32)
+    over the selected blocks ids [B, S, topk].
+
+    cap > 0 caps the scaled scores z at cap * tanh(z / cap); slopes [H_q] fp32
+    subtracts slopes[h] * |p - t|; first / last [B, S] int32 bound the tokens a
+    query attends (document mask: first = its document's start; prefix mask:
+    last = max(p, prefix - 1)). lse and mass are True or output tensors: the
+    base-2 log-sum-exp [B, S, H_q], and the softmax weight each selected block
+    received [B, S, H_kv, topk], summed over the KV head's query heads.
+    Returns out, or (out[, lse][, mass]) with those asked for."""
+    return prepare_sparse_attn_q8(q, cache, table, ids, ctx_len, q_start, scale, cap, slopes, first,
+                                  last, phase, out, lse, mass)(stream)
+
+
+def prepare_block_weight_update(weight: torch.Tensor, ids: torch.Tensor, mass: torch.Tensor,
+                                decay: float = 1.0) -> PreparedCall:
+    """block_weight_update as a PreparedCall."""
+    if weight.dim() != 2 or ids.dim() != 3 or mass.dim() != 4:
+        raise ValueError("lci: weight must be [B, NB], ids [B, S, topk], mass [B, S, H_kv, topk]")
+    B, NB = weight.shape
+    S, H_kv, topk = mass.shape[1:]
+    dev = _one_device(weight, ids, mass)
+    args = (_shaped(ids, "ids", torch.int32, (B, S, topk)),
+            _shaped(mass, "mass", torch.float32, (B, S, H_kv, topk)), B, S, H_kv, topk, NB,
+            float(decay), _dev(weight, "weight", torch.float32, 2))
+    return PreparedCall("lci_block_weight_update", args, (weight,), dev, (weight, ids, mass))
+
+
+def block_weight_update(weight: torch.Tensor, ids: torch.Tensor, mass: torch.Tensor,
+                        decay: float = 1.0, stream=None) -> torch.Tensor:
+    """weight[b, j] = decay * weight[b, j] + the mass that block j received
+    (ids [B, S, topk], mass [B, S, H_kv, topk] of sparse_attn_q8), in place.
+    Returns weight [B, NB] fp32."""
+    return prepare_block_weight_update(weight, ids, mass, decay)(stream)[0]
+
+
+def prepare_cache_evict(table: BlockTable, ctx_len: torch.Tensor, weight: torch.Tensor, budget: int,
+                        sink: int = 0, recent: int = 1, in_place: bool = False) -> PreparedCall:
+    """cache_evict as a PreparedCall."""
+    if weight.dim() != 2:
+        raise ValueError("lci: weight must be [B, max_blocks]")
+    B, NB = weight.shape
+    if NB != table.max_blocks:
+        raise ValueError("lci: weight must be [B, max_blocks]")
+    if B > table.batch:
+        raise ValueError("lci: weight has more sequences than the block table")
+    dev = _one_device(table.table, ctx_len, weight)
+    pt = _dev(table.table, "block_table", torch.int32, 2)
+    pc = _shaped(ctx_len, "ctx_len", torch.int32, (B,))
+    pw = _dev(weight, "weight", torch.float32, 2)
+    if in_place:
+        new = (table.table, ctx_len, weight)
+    else:
+        new = (torch.empty((B, NB), dtype=torch.int32, device=dev), torch.empty_like(ctx_len),
+               torch.empty_like(weight))
+    kept = torch.empty((B, max(int(budget), 0)), dtype=torch.int32, device=dev)
+    freed = torch.empty((B,), dtype=torch.int32, device=dev)
+    args = (table.handle, B, pc, pw, int(budget), int(sink), int(recent),
+            *(ctypes.c_void_p(t.data_ptr()) for t in new + (kept, freed)))
+    return PreparedCall("lci_cache_evict", args, new + (kept, freed), dev,
+                        (table, ctx_len, weight) + new + (kept, freed))
+
+
+def cache_evict(table: BlockTable, ctx_len: torch.Tensor, weight: torch.Tensor, budget: int,
+                sink: int = 0, recent: int = 1, in_place: bool = True, stream=None):
+    """Trim every sequence to ``budget`` blocks: the first ``sink``, the last
+    ``recent`` and the heaviest of the rest stay, in order; freed pages follow
+    the kept ones in the table row. Returns (table [B, NB], ctx_len [B], weight
+    [B, NB], kept [B, budget] old block ids, freed [B]); in place these are the
+    block table's own tensor, ctx_len and weight."""
+    return prepare_cache_evict(table, ctx_len, weight, budget, sink, recent, in_place)(stream)
 
 
 def sparse_attn_pipelined(q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,

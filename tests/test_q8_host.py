@@ -1,0 +1,164 @@
+"""The 8-bit cache's entry points refuse bad arguments on the host, and the
+64-bit reference of their tests is right (CPU only: no CUDA call is reached)."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import long_context_indexer_b200 as lci
+from long_context_indexer_b200.build import build
+
+from . import q8_reference as ref
+
+INVALID, UNSUPPORTED = 1, 2
+FAKE = ctypes.c_void_p(0x7F0000000000)
+ODD = ctypes.c_void_p(0x7F0000000008)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build()
+    return lci.load_library()
+
+
+@pytest.fixture(scope="module")
+def tables(lib):
+    made = {}
+    for name, (nb, P, bs, H, hd, dt) in dict(
+            q8=(4, 8, 64, 2, 128, 2), bf16=(4, 8, 64, 2, 128, 1), odd=(4, 8, 64, 2, 48, 2),
+            wide=(4, 8, 64, 2, 288, 2), long=(1 << 15, 8, 64, 2, 128, 2),
+            huge=(1 << 25, 8, 64, 2, 128, 2)).items():
+        h = ctypes.c_void_p()
+        assert lib.lci_create_block_table(FAKE, 2, nb, P, bs, H, hd, dt, ctypes.byref(h)) == 0
+        made[name] = h
+    yield made
+    for h in made.values():
+        lib.lci_destroy_block_table(h)
+
+
+def test_other_attention_refuses_an_e4m3_table(lib, tables):
+    assert lib.lci_sparse_attn(FAKE, 2, 1, 16, FAKE, FAKE, tables["q8"], FAKE, 4, FAKE, FAKE, 0.0, 0,
+                               FAKE, None, 0, None) == UNSUPPORTED
+    assert lib.lci_sparse_attn_partial(FAKE, 2, 1, 16, FAKE, FAKE, tables["q8"], FAKE, 4, FAKE, FAKE,
+                                       0.0, 0, FAKE, FAKE, None) == UNSUPPORTED
+    assert lib.lci_sparse_attn_pipelined(FAKE, 2, 1, 16, FAKE, FAKE, tables["q8"], FAKE, 4, FAKE,
+                                         FAKE, 0.0, FAKE, FAKE, None) == UNSUPPORTED
+    n = ctypes.c_size_t()
+    assert lib.lci_sparse_decode_workspace_size(2, 1, 8, 128, 4, 16, tables["q8"],
+                                                ctypes.byref(n)) != 0
+    for fn in (lib.lci_sparse_decode, lib.lci_sparse_decode_persistent):
+        for dtype in (0, 1, 2):
+            assert fn(FAKE, FAKE, dtype, 2, 1, 8, 128, 4, FAKE, FAKE, 4, FAKE, 16, FAKE, FAKE,
+                      tables["q8"], 0.0, FAKE, FAKE, FAKE, 1 << 30, None) in (INVALID, UNSUPPORTED)
+    h = ctypes.c_void_p()
+    assert lib.lci_create_block_table(FAKE, 2, 4, 8, 64, 2, 128, 3, ctypes.byref(h)) == INVALID
+
+
+def test_kv_append_q8_refusals(lib, tables):
+    def call(**kw):
+        a = dict(k=FAKE, v=FAKE, dtype=1, B=2, T=1, start=FAKE, count=None, t=tables["q8"], kp=FAKE,
+                 vp=FAKE, ks=FAKE, vs=FAKE)
+        a.update(kw)
+        return lib.lci_kv_append_q8(*a.values(), None)
+    for name in ("k", "v", "start", "kp", "vp", "ks", "vs", "t"):
+        assert call(**{name: None}) == INVALID, name
+    assert call(B=0) == INVALID and call(B=3) == INVALID and call(T=0) == INVALID
+    assert call(dtype=2) == INVALID and call(dtype=9) == INVALID
+    assert call(t=tables["bf16"]) == INVALID
+    assert call(kp=ODD) == INVALID and call(vp=ODD) == INVALID
+
+
+def test_sparse_attn_q8_refusals(lib, tables):
+    class Opt(ctypes.Structure):
+        _fields_ = [("cap", ctypes.c_float), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                    ("c", ctypes.c_void_p)]
+
+    def call(**kw):
+        a = dict(q=FAKE, dtype=1, B=2, S=1, Hq=16, kp=FAKE, vp=FAKE, ks=FAKE, vs=FAKE,
+                 t=tables["q8"], ids=FAKE, topk=4, ctx=FAKE, q0=FAKE, scale=0.0, opt=None, phase=0,
+                 out=FAKE, lse=None, mass=None)
+        a.update(kw)
+        return lib.lci_sparse_attn_q8(*a.values(), None)
+    for name in ("q", "kp", "vp", "ks", "vs", "t", "ids", "ctx", "q0", "out"):
+        assert call(**{name: None}) == INVALID, name
+    assert call(S=0) == INVALID and call(Hq=15) == INVALID and call(topk=0) == INVALID
+    assert call(B=3) == INVALID and call(dtype=2) == INVALID and call(phase=3) == INVALID
+    assert call(t=tables["bf16"]) == INVALID
+    assert call(q=ODD) == INVALID and call(out=ODD) == INVALID and call(vp=ODD) == INVALID
+    assert call(scale=float("inf")) == INVALID
+    for cap in (-1.0, float("nan"), float("inf")):
+        assert call(opt=ctypes.byref(Opt(cap, None, None, None))) == INVALID
+    assert call(topk=257) == UNSUPPORTED
+    assert call(t=tables["odd"]) == UNSUPPORTED and call(t=tables["wide"]) == UNSUPPORTED
+    assert call(t=tables["huge"]) == UNSUPPORTED
+
+
+def test_block_weight_update_refusals(lib):
+    def call(**kw):
+        a = dict(ids=FAKE, mass=FAKE, B=2, S=1, H=1, topk=4, NB=16, decay=1.0, w=FAKE)
+        a.update(kw)
+        return lib.lci_block_weight_update(*a.values(), None)
+    for name in ("ids", "mass", "w"):
+        assert call(**{name: None}) == INVALID
+    for name in ("B", "S", "H", "topk", "NB"):
+        assert call(**{name: 0}) == INVALID
+    for decay in (-0.5, float("nan"), float("inf")):
+        assert call(decay=decay) == INVALID
+    assert call(topk=257) == UNSUPPORTED and call(NB=16385) == UNSUPPORTED
+
+
+def test_cache_evict_refusals(lib, tables):
+    def call(**kw):
+        a = dict(t=tables["q8"], B=2, ctx=FAKE, w=FAKE, budget=3, sink=1, recent=1, to=FAKE, co=FAKE,
+                 wo=FAKE, kept=None, freed=None)
+        a.update(kw)
+        return lib.lci_cache_evict(*a.values(), None)
+    for name in ("t", "ctx", "w", "to", "co", "wo"):
+        assert call(**{name: None}) == INVALID
+    assert call(B=0) == INVALID and call(B=3) == INVALID
+    assert call(sink=-1) == INVALID and call(recent=0) == INVALID
+    assert call(sink=2, recent=2) == INVALID and call(budget=0) == INVALID
+    assert call(t=tables["long"]) == UNSUPPORTED
+
+
+def test_binding_refuses_cpu_tensors():
+    with pytest.raises(ValueError):
+        lci.block_weight_update(torch.zeros(1, 4), torch.zeros(1, 1, 2, dtype=torch.int32),
+                                torch.zeros(1, 1, 1, 2))
+
+
+# ---------------------------------------------------------------- the reference
+
+def test_reference_rounds_to_e4m3_like_torch():
+    g = torch.Generator().manual_seed(0)
+    x = torch.cat([torch.randn(4000, generator=g) * s for s in (1e-3, 0.01, 1.0, 100.0)]).clamp(-448, 448)
+    mid = ((ref.E4M3[1:] + ref.E4M3[:-1]) / 2).float()  # ties
+    x = torch.cat([x, mid, -mid, ref.E4M3.float(), torch.zeros(1)])
+    assert torch.equal(ref.e4m3_round(x.double()).float(), x.to(torch.float8_e4m3fn).float())
+
+
+@pytest.mark.parametrize("amax", [448.0, 448.0001, 1.0, 3.5, 1.75, 1e-30, 0.0, 3e38])
+def test_reference_scale_is_the_smallest_that_fits(amax):
+    s = ref.needed_scale(amax)
+    assert math.log2(s) == int(math.log2(s)) and s >= 2.0 ** -60 and 448 * s >= amax
+    assert s == 2.0 ** -60 or 448 * s / 2 < amax
+
+
+def test_reference_attention_is_dense_attention():
+    g = torch.Generator().manual_seed(1)
+    bs, H, hd, n = 4, 2, 8, 11
+    k = torch.randn(5, H, bs, hd, generator=g).to(torch.float8_e4m3fn)
+    v = torch.randn(5, H, bs, hd, generator=g).to(torch.float8_e4m3fn)
+    ks, vs = torch.rand(5, H, generator=g) + 0.5, torch.rand(5, H, generator=g) + 0.5
+    table = torch.tensor([[3, 0, 4]], dtype=torch.int32)
+    q = torch.randn(1, n, 4, hd, generator=g)
+    ids = torch.tensor([2, 0, 1], dtype=torch.int32).repeat(1, n, 1)
+    out, lse, mass, _ = ref.attend(q.double(), k.double(), v.double(), ks, vs, table, bs, ids,
+                                   torch.tensor([n]), torch.tensor([0]))
+    K = (k.double() * ks.double()[:, :, None, None])[table[0].long()].transpose(0, 1).reshape(H, -1, hd)[:, :n]
+    V = (v.double() * vs.double()[:, :, None, None])[table[0].long()].transpose(0, 1).reshape(H, -1, hd)[:, :n]
+    want = torch.nn.functional.scaled_dot_product_attention(
+        q[0].transpose(0, 1).double(), K.repeat_interleave(2, 0), V.repeat_interleave(2, 0), is_causal=True)
+    assert torch.allclose(out[0].transpose(0, 1), want, atol=1e-12)
+    assert torch.allclose(mass.sum(-1), torch.full((1, n, H), 2.0, dtype=torch.float64))
