@@ -1,0 +1,541 @@
+// attn_q8_rows.cuh -- row-wise attention over the 8-bit paged cache: bf16
+// queries, head_dim 64 or 128, block_size a multiple of 16, up to 16 query
+// heads per KV head. Decode steps, and prompts whose queries share few blocks.
+//
+// Work: one "pair" = (query row, KV head). Its selected blocks are cut into
+// strips of 16 tokens. The CTAs of a cluster take whole blocks, the warps of a
+// CTA equal runs of its strips, and every warp runs alone: it loads a strip's K
+// and V straight from global memory into the registers its MMA fragments need
+// (16-byte loads that cover whole 128-byte rows; the next strip is in flight
+// while one is computed), converts the codes to f16 (exact), and keeps its own
+// running maximum, sum and O. No shared memory, barrier or copy engine sits in
+// the loop, so the bytes in flight are the warps' registers (8 KiB a warp) and
+// the first load waits for nothing but the page lookup.
+//
+// Arithmetic. mma.m16n8k16, f16 in and fp32 out; the 16 rows are the group's
+// query heads. A query row is scaled by a power of two so that its largest
+// element is in [2^14, 2^15): every bf16 element down to 2^-29 of the largest
+// is then exact in f16 (smaller ones are off by less than 2^-40 of it). A
+// block's k scale multiplies the fp32 logits. With the v scale = f * 2^e,
+// f in [1, 2), the weight p = 2^(x + e - m) carries e, so that p is the
+// weight of the *codes* and m the running maximum of x + e; p * f is rounded to
+// f16 (11 bits) for P V, and the row sum adds p * 2^-e. The reference m moves
+// only when a strip passes it by more than 8, so O is rarely rescaled and
+// p <= 2^8.
+//
+// Fragment layout: a lane's 16-byte run of K holds 16 dims of one token, four
+// k-steps of B; the query's dims are permuted alike. For V, lane (g, q) loads
+// dims g * HD/8 .. of tokens 2q, 2q+1, 2q+8, 2q+9; bytes of two tokens are
+// paired by a byte permute and converted together.
+#pragma once
+
+#include <cooperative_groups.h>
+
+#include "attn_q8_simt.cuh"
+#include "common.cuh"
+#include "ptx.cuh"
+#include "q8_cache.cuh"
+
+namespace lci {
+
+namespace q8r {
+constexpr int kStrip = 16;
+constexpr int kRows = 16;       // query heads per MMA (padded)
+constexpr int kMaxSplit = 8;
+constexpr float kLazy = 8.f;
+// shared memory, in floats. O rows: four segments of HD/4 dims, each padded by 8
+// and the row by 4, so that 8 lanes' 16-byte stores meet 32 different banks.
+template <int HD> __host__ __device__ constexpr int seg_pitch() { return HD / 4 + 8; }
+template <int HD> __host__ __device__ constexpr int row_pitch() { return HD + 32 + 4; }
+template <int HD, int NW> __host__ __device__ constexpr int o_floats() { return NW * kRows * row_pitch<HD>(); }
+template <int HD, int NW> __host__ __device__ constexpr int base_floats() {
+    return o_floats<HD, NW>() + NW * kRows * 2 /*warps' max, sum*/ +
+           kRows * HD + 4 * kMaxSplit /*slices received*/ +
+           kMaxSplit * kRows * 2 /*CTAs' max, sum*/;
+}
+// (max, sum) per head of each (block, warp) that meet: blocks + warps entries
+template <int HD, int NW>
+__host__ __device__ constexpr size_t smem_bytes(int blocks_with_mass) {
+    return (size_t)(base_floats<HD, NW>() +
+                    (blocks_with_mass ? (blocks_with_mass + NW) * kRows * 2 : 0)) * 4;
+}
+}  // namespace q8r
+
+// D += A(16x16, row) * B(16x8, col), f16 inputs, fp32 accumulators.
+__device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A v scale as f * 2^e, f in [1, 2); below 2^-60 it counts as 2^-60.
+struct VScale {
+    float f, e, inv;  // inv = 2^-e
+};
+__device__ __forceinline__ VScale split_v_scale(float vs) {
+    vs = fmaxf(vs, kMinVScale);
+    const uint32_t u = __float_as_uint(vs);
+    const int e = (int)(u >> 23) - 127;
+    VScale r;
+    r.f = __uint_as_float((u & 0x7fffffu) | 0x3f800000u);
+    r.e = (float)e;
+    r.inv = __uint_as_float((uint32_t)(127 - e) << 23);
+    return r;
+}
+
+// One strip's raw codes, as this lane's MMA fragments need them.
+template <int HD>
+struct Q8Strip {
+    uint4 k[2][HD / 64];        // [8-token half][16-byte run]
+    uint32_t v[4][HD / 32];     // [token 2q, 2q+1, 2q+8, 2q+9][words]
+    __device__ __forceinline__ void load(const uint8_t* kp, const uint8_t* vp, int g8, int q4) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int c = 0; c < HD / 64; ++c)
+                k[j][c] = __ldg(reinterpret_cast<const uint4*>(kp + (8 * j + g8) * HD + 16 * (q4 + 4 * c)));
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const uint8_t* p = vp + (2 * q4 + (t & 1) + 8 * (t >> 1)) * HD + g8 * (HD / 8);
+            if constexpr (HD == 128) {
+                const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
+                v[t][0] = x.x;
+                v[t][1] = x.y;
+                v[t][2] = x.z;
+                v[t][3] = x.w;
+            } else {
+                const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
+                v[t][0] = x.x;
+                v[t][1] = x.y;
+            }
+        }
+    }
+};
+
+template <int HD, int NW, bool MODS>
+__global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_kernel(
+    const __grid_constant__ AttnQ8Args a, int nsplit) {
+    using namespace q8r;
+    namespace cg = cooperative_groups;
+    constexpr int NT = NW * 32;
+    constexpr int KS = HD / 16;  // k-steps of Q K^T
+    constexpr int ON = HD / 8;   // n-tiles of O
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    float* so = reinterpret_cast<float*>(smem_raw);       // [NW][16][row_pitch]
+    float* sml = so + o_floats<HD, NW>();                 // [NW][16][max, sum]
+    float* recv = sml + NW * kRows * 2;                   // this CTA's slice, from each CTA
+    float* cml = recv + kRows * HD + 4 * kMaxSplit;       // [CTA][16][max, sum]
+    float* sbm = cml + kMaxSplit * kRows * 2;             // [block + warp][16][max, sum]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g8 = lane >> 2, q4 = lane & 3;
+    const int split = blockIdx.x % nsplit;
+    const long long pair = blockIdx.x / nsplit;
+    const int row = (int)(pair / a.H_kv), g = (int)(pair - (long long)row * a.H_kv);
+    const int G = a.H_q / a.H_kv;
+    const int b = row / a.S, s = row - b * a.S;
+    const int spb = a.bs / kStrip;  // strips per block
+    // this CTA's blocks, this warp's strips of them
+    const int per = (a.topk + nsplit - 1) / nsplit;
+    const int i0 = min(a.topk, split * per), nblk = min(a.topk, i0 + per) - i0;
+    const int nstrips = nblk * spb;
+    const int wper = (nstrips + NW - 1) / NW;
+    const int w0 = min(nstrips, warp * wper), w1 = min(nstrips, w0 + wper);
+
+    pdl_wait();  // nothing of global memory is read before
+    if (nsplit > 1) cluster_arrive_relaxed();  // matched before the first remote store
+    const bool mass = a.mass != nullptr;
+    if (mass) {
+        for (int e = tid; e < (nblk + NW) * kRows; e += NT)
+            *reinterpret_cast<float2*>(sbm + 2 * e) = make_float2(-INFINITY, 0.f);
+        __syncthreads();
+    }
+
+    // the group's query rows, scaled to f16 (head rows g8 and g8 + 8)
+    uint32_t qf[KS][4];
+    float qs_a, qs_b;  // what a row's logits are multiplied by (with the softmax scale)
+    {
+        const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(a.q) + ((size_t)row * a.H_q + (size_t)g * G) * HD;
+        float back[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int h = g8 + 8 * r;
+            uint4 w[HD / 64][2];
+            float amax = 0.f;
+#pragma unroll
+            for (int c = 0; c < HD / 64; ++c)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    w[c][x] = h < G ? __ldg(reinterpret_cast<const uint4*>(qrow + (size_t)h * HD + 16 * (q4 + 4 * c) + 8 * x))
+                                    : make_uint4(0, 0, 0, 0);
+                    const uint32_t u[4] = {w[c][x].x, w[c][x].y, w[c][x].z, w[c][x].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 f = bf16x2_to_f32(u[k]);
+                        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // 2^(14 - exponent of amax), its inverse multiplies the logits
+            int e = (int)(__float_as_uint(amax) >> 23) - 127;
+            e = e < -100 ? -100 : e > 127 ? 127 : e;
+            const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
+            back[r] = __uint_as_float((uint32_t)(e - 14 + 127) << 23);
+#pragma unroll
+            for (int c = 0; c < HD / 64; ++c)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t u[4] = {w[c][x].x, w[c][x].y, w[c][x].z, w[c][x].w};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {  // k-step 4c + 2x + k: dims 4k .. 4k+3 of the run's half
+                        const float2 lo = bf16x2_to_f32(u[2 * k]), hi = bf16x2_to_f32(u[2 * k + 1]);
+                        qf[4 * c + 2 * x + k][r] = pack_f16x2(lo.x * up, lo.y * up);
+                        qf[4 * c + 2 * x + k][2 + r] = pack_f16x2(hi.x * up, hi.y * up);
+                    }
+                }
+        }
+        const float unit = MODS ? a.scale : a.scale * kLog2e;
+        qs_a = unit * back[0];
+        qs_b = unit * back[1];
+    }
+    const Q8Window win = q8_window(a, row, b, s);
+    float slope_a = 0.f, slope_b = 0.f, inv_cap = 0.f;
+    if constexpr (MODS) {
+        inv_cap = a.cap > 0.f ? 1.f / a.cap : 0.f;
+        if (a.slopes) {
+            slope_a = g8 < G ? a.slopes[g * G + g8] : 0.f;
+            slope_b = g8 + 8 < G ? a.slopes[g * G + g8 + 8] : 0.f;
+        }
+    }
+
+    float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;  // l: this lane's share
+    float r_a = 0.f, r_b = 0.f;                                    // the current block's share
+    float o[ON][4];
+#pragma unroll
+    for (int i = 0; i < ON; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+
+    // (max, sum) of the block just finished, for its mass
+    auto close_block = [&](int blk) {
+        if (!mass) return;
+        float x = r_a, y = r_b;
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        y += __shfl_xor_sync(0xffffffffu, y, 1);
+        y += __shfl_xor_sync(0xffffffffu, y, 2);
+        if (q4 == 0) {
+            float2* d = reinterpret_cast<float2*>(sbm) + (size_t)(blk + warp) * kRows;
+            d[g8] = make_float2(m_a, x);
+            d[g8 + 8] = make_float2(m_b, y);
+        }
+        r_a = r_b = 0.f;
+    };
+
+    const int32_t* row_ids = a.ids + (size_t)row * a.topk + i0;
+    const int blk_end = w1 > w0 ? (w1 - 1) / spb + 1 : 0;
+    // blocks of this warp in batches of 32: lanes look up pages and scales
+    for (int base = w1 > w0 ? w0 / spb : 0; base < blk_end; base += 32) {
+        int t_lane = -1;
+        size_t cell = 0;
+        float ks = 0.f, vs = 0.f;
+        if (base + lane < blk_end) {
+            const int j = row_ids[base + lane];
+            const int page = q8_page(a, b, j, win);
+            if (page >= 0) {
+                t_lane = j * a.bs;
+                cell = (size_t)page * a.H_kv + g;
+                ks = a.ks[cell];
+                vs = a.vs[cell];
+            }
+        }
+        uint32_t live = __ballot_sync(0xffffffffu, t_lane >= 0);
+        if (live == 0u) continue;
+        // block, strip and pointers of the load cursor, one strip ahead of the compute
+        int blk = -1, st = 0, st_end = 0;
+        const uint8_t *kp = nullptr, *vp = nullptr;
+        int t_first = 0;
+        auto enter = [&](int x) {  // strip range and pointers of batch entry x
+            blk = x;
+            const int first = (base + x) * spb;
+            t_first = __shfl_sync(0xffffffffu, t_lane, x);
+            const unsigned long long c = __shfl_sync(0xffffffffu, (unsigned long long)cell, x);
+            kp = a.k + c * a.bs * HD;
+            vp = a.v + c * a.bs * HD;
+            // strips of this warp, cut to the window
+            st = max(w0 - first, 0);
+            st_end = min(w1 - first, spb);
+            const int lo = win.lo - t_first, hi = win.hi - t_first;
+            if (lo > 0) st = max(st, lo / kStrip);
+            st_end = min(st_end, hi / kStrip + 1);
+        };
+        auto next_block = [&]() -> bool {  // to the first strip of the next live block
+            while (live) {
+                const int x = __ffs(live) - 1;
+                live &= live - 1u;
+                enter(x);
+                if (st < st_end) return true;
+            }
+            return false;
+        };
+        Q8Strip<HD> cur, nxt;
+        bool have = next_block();
+        if (have) cur.load(kp + (size_t)st * kStrip * HD, vp + (size_t)st * kStrip * HD, g8, q4);
+        while (have) {
+            const int c_blk = blk, c_t0 = t_first + st * kStrip;
+            bool more = true;
+            ++st;
+            if (st >= st_end) more = next_block();
+            if (more) nxt.load(kp + (size_t)st * kStrip * HD, vp + (size_t)st * kStrip * HD, g8, q4);
+            const float c_ks = __shfl_sync(0xffffffffu, ks, c_blk);
+            const VScale c_vs = split_v_scale(__shfl_sync(0xffffffffu, vs, c_blk));
+
+            // S = Q K^T: two n-tiles of 8 tokens
+            float sc[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[j][e] = 0.f;
+#pragma unroll
+                for (int c = 0; c < HD / 64; ++c) {
+                    const uint32_t w[4] = {cur.k[j][c].x, cur.k[j][c].y, cur.k[j][c].z, cur.k[j][c].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_f16_16816(sc[j], qf[4 * c + k], e4m3x2_to_f16x2(w[k]), e4m3x2_to_f16x2(w[k] >> 16));
+                }
+            }
+            // logits in log2 units, plus the v scale's exponent
+            const float ca = qs_a * c_ks, cb = qs_b * c_ks;
+            float x[2][4];
+            const int ta = c_t0 + 2 * q4;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float z = sc[j][e] * (e < 2 ? ca : cb);
+                    if constexpr (MODS)
+                        x[j][e] = q8_score(z, a.cap, inv_cap, e < 2 ? slope_a : slope_b,
+                                           abs(win.p - (ta + 8 * j + (e & 1)))) + c_vs.e;
+                    else
+                        x[j][e] = z + c_vs.e;
+                }
+            const bool partial = c_t0 < win.lo || c_t0 + kStrip - 1 > win.hi;
+            if (partial) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int t = ta + 8 * j + e;
+                        if (t < win.lo || t > win.hi) {
+                            x[j][e] = x[j][e + 2] = -INFINITY;
+#pragma unroll
+                            for (int w = 0; w < HD / 32; ++w) cur.v[2 * j + e][w] = 0u;  // unset memory
+                        }
+                    }
+            }
+            float mx_a = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
+            float mx_b = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
+            mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 1));
+            mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, 1));
+            mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 2));
+            mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, 2));
+            const bool up_a = mx_a > m_a + kLazy, up_b = mx_b > m_b + kLazy;
+            if (__any_sync(0xffffffffu, up_a || up_b)) {
+                const float co_a = up_a ? exp2f(m_a - mx_a) : 1.f, co_b = up_b ? exp2f(m_b - mx_b) : 1.f;
+                m_a = up_a ? mx_a : m_a;
+                m_b = up_b ? mx_b : m_b;
+                l_a *= co_a;
+                l_b *= co_b;
+                r_a *= co_a;
+                r_b *= co_b;
+#pragma unroll
+                for (int i = 0; i < ON; ++i) {
+                    o[i][0] *= co_a;
+                    o[i][1] *= co_a;
+                    o[i][2] *= co_b;
+                    o[i][3] *= co_b;
+                }
+            }
+            const float base_a = m_a == -INFINITY ? 0.f : m_a, base_b = m_b == -INFINITY ? 0.f : m_b;
+            float p[2][4], sum_a = 0.f, sum_b = 0.f;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                p[j][0] = fast_exp2(x[j][0] - base_a);
+                p[j][1] = fast_exp2(x[j][1] - base_a);
+                p[j][2] = fast_exp2(x[j][2] - base_b);
+                p[j][3] = fast_exp2(x[j][3] - base_b);
+                sum_a += p[j][0] + p[j][1];
+                sum_b += p[j][2] + p[j][3];
+            }
+            sum_a *= c_vs.inv;
+            sum_b *= c_vs.inv;
+            l_a += sum_a;
+            l_b += sum_b;
+            r_a += sum_a;
+            r_b += sum_b;
+            uint32_t pf[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                pf[2 * j] = pack_f16x2(p[j][0] * c_vs.f, p[j][1] * c_vs.f);
+                pf[2 * j + 1] = pack_f16x2(p[j][2] * c_vs.f, p[j][3] * c_vs.f);
+            }
+            // O += P V
+#pragma unroll
+            for (int w = 0; w < HD / 32; ++w) {
+                const uint32_t ab0 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x5140);
+                const uint32_t ab1 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x7362);
+                const uint32_t cd0 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x5140);
+                const uint32_t cd1 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x7362);
+                mma_f16_16816(o[4 * w], pf, e4m3x2_to_f16x2(ab0), e4m3x2_to_f16x2(cd0));
+                mma_f16_16816(o[4 * w + 1], pf, e4m3x2_to_f16x2(ab0 >> 16), e4m3x2_to_f16x2(cd0 >> 16));
+                mma_f16_16816(o[4 * w + 2], pf, e4m3x2_to_f16x2(ab1), e4m3x2_to_f16x2(cd1));
+                mma_f16_16816(o[4 * w + 3], pf, e4m3x2_to_f16x2(ab1 >> 16), e4m3x2_to_f16x2(cd1 >> 16));
+            }
+            if (!more || blk != c_blk) close_block(base + c_blk);
+            have = more;
+            cur = nxt;
+        }
+    }
+
+    // ---- the warps' partials: (max, sum) and O in shared memory ----
+    l_a += __shfl_xor_sync(0xffffffffu, l_a, 1);
+    l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
+    l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
+    l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
+    if (q4 == 0) {
+        float2* d = reinterpret_cast<float2*>(sml) + warp * kRows;
+        d[g8] = make_float2(m_a, l_a);
+        d[g8 + 8] = make_float2(m_b, l_b);
+    }
+    {
+        // lane (g8, q4) holds dims q4 * HD/4 .. of head rows g8 and g8 + 8
+        float* d = so + warp * kRows * row_pitch<HD>() + g8 * row_pitch<HD>() + q4 * seg_pitch<HD>();
+#pragma unroll
+        for (int c = 0; c < 2; ++c)  // component: dims c * HD/8 .. of the segment
+#pragma unroll
+            for (int i = 0; i < ON; i += 4) {
+                *reinterpret_cast<float4*>(d + c * ON + i) =
+                    make_float4(o[i][c], o[i + 1][c], o[i + 2][c], o[i + 3][c]);
+                *reinterpret_cast<float4*>(d + 8 * row_pitch<HD>() + c * ON + i) =
+                    make_float4(o[i][2 + c], o[i + 1][2 + c], o[i + 2][2 + c], o[i + 3][2 + c]);
+            }
+    }
+    __syncthreads();
+    if (nsplit > 1) cluster_wait();  // every CTA of the cluster runs
+    const int groups = G * (HD / 4);  // float4 groups of the pair's output
+    const int share = (groups + nsplit - 1) / nsplit;
+    __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) + ((size_t)row * a.H_q + (size_t)g * G) * HD;
+    auto merged = [&](const float* ml, int n, int h, float& M) -> float {  // max and sum over n partials
+        M = -INFINITY;
+        for (int w = 0; w < n; ++w) M = fmaxf(M, ml[(w * kRows + h) * 2]);
+        const float base = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+        for (int w = 0; w < n; ++w) L += exp2f(ml[(w * kRows + h) * 2] - base) * ml[(w * kRows + h) * 2 + 1];
+        return L;
+    };
+    auto write4 = [&](int q, float4 v, float L) {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        uint2 w = make_uint2(0u, 0u);
+        if (L != 0.f) {
+            w.x = pack_bf16x2(v.x * inv, v.y * inv);
+            w.y = pack_bf16x2(v.z * inv, v.w * inv);
+        }
+        *reinterpret_cast<uint2*>(orow + 4 * q) = w;
+    };
+    for (int q = tid; q < groups; q += NT) {
+        const int h = q / (HD / 4), c = q - h * (HD / 4);
+        const int seg = c / (HD / 16), in = c - seg * (HD / 16);
+        const float* src = so + h * row_pitch<HD>() + seg * seg_pitch<HD>() + 4 * in;
+        float M;
+        const float L = merged(sml, NW, h, M);
+        const float base = M == -INFINITY ? 0.f : M;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float f = exp2f(sml[(w * kRows + h) * 2] - base);
+            const float4 v = *reinterpret_cast<const float4*>(src + w * kRows * row_pitch<HD>());
+            acc.x += f * v.x;
+            acc.y += f * v.y;
+            acc.z += f * v.z;
+            acc.w += f * v.w;
+        }
+        if (nsplit == 1) {
+            write4(q, acc, L);
+        } else {
+            const int owner = q / share;
+            float* dst = cg::this_cluster().map_shared_rank(recv, owner) + (size_t)(split * share + q - owner * share) * 4;
+            *reinterpret_cast<float4*>(dst) = acc;
+        }
+    }
+    const float* ml = sml;  // partials the pair's max and sum come from
+    int nml = NW;
+    if (nsplit > 1) {
+        if (tid < G * nsplit) {  // this CTA's (max, sum) to every CTA
+            const int h = tid % G, to = tid / G;
+            float M;
+            const float L = merged(sml, NW, h, M);
+            float* dst = cg::this_cluster().map_shared_rank(cml, to) + (split * kRows + h) * 2;
+            *reinterpret_cast<float2*>(dst) = make_float2(M, L);
+        }
+        cluster_arrive();
+        cluster_wait();
+        ml = cml;
+        nml = nsplit;
+        for (int q = split * share + tid; q < min(groups, (split + 1) * share); q += NT) {
+            const int h = q / (HD / 4);
+            float M;
+            const float L = merged(cml, nsplit, h, M);
+            const float base = M == -INFINITY ? 0.f : M;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int r = 0; r < nsplit; ++r) {
+                const float f = exp2f(cml[(r * kRows + h) * 2] - base);
+                const float4 v = *reinterpret_cast<const float4*>(recv + (size_t)(r * share + q - split * share) * 4);
+                acc.x += f * v.x;
+                acc.y += f * v.y;
+                acc.z += f * v.z;
+                acc.w += f * v.w;
+            }
+            write4(q, acc, L);
+        }
+    }
+    if (a.lse && split == 0 && tid < G) {
+        float M;
+        const float L = merged(ml, nml, tid, M);
+        a.lse[(size_t)row * a.H_q + (size_t)g * G + tid] = L == 0.f ? -INFINITY : M + log2f(L);
+    }
+    if (mass) {
+        // mass of block i: over the warps that met it and the group's heads
+        float* mrow = a.mass + ((size_t)row * a.H_kv + g) * a.topk + i0;
+        for (int e = tid; e < nblk * 4; e += NT) {  // four lanes share a block's heads
+            const int i = e >> 2, part = e & 3;
+            const uint32_t quad = 0xfu << (lane & 28);
+            float x = 0.f;
+            if (wper > 0) {
+                const int wa = (i * spb) / wper, wb = min(NW - 1, (i * spb + spb - 1) / wper);
+                for (int h = part; h < G; h += 4) {
+                    float M;
+                    const float L = merged(ml, nml, h, M);
+                    if (L == 0.f) continue;
+                    const float base = M == -INFINITY ? 0.f : M;
+                    float y = 0.f;
+                    for (int w = wa; w <= wb; ++w) {
+                        const float2 v = *(reinterpret_cast<const float2*>(sbm) + (size_t)(i + w) * kRows + h);
+                        y += exp2f(v.x - base) * v.y;
+                    }
+                    x += y / L;
+                }
+            }
+            x += __shfl_xor_sync(quad, x, 1);
+            x += __shfl_xor_sync(quad, x, 2);
+            if (part == 0) mrow[i] = x;
+        }
+    }
+}
+
+}  // namespace lci

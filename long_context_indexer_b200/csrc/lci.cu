@@ -17,6 +17,7 @@
 #include "../../include/lci.h"
 #include "attn_decode.cuh"
 #include "attn_prefill.cuh"
+#include "attn_q8_rows.cuh"
 #include "attn_q8_simt.cuh"
 #include "attn_simt.cuh"
 #include "cache_evict.cuh"
@@ -1437,6 +1438,61 @@ lci_status launch_attn_q8_simt(const lci::AttnQ8Args& a, int32_t batch, cudaStre
     return check_launch("sparse_attn_q8");
 }
 
+// The row-wise tensor-core schedule (attn_q8_rows.cuh).
+bool rows_q8_fits(const lci::AttnQ8Args& a, lci_dtype dtype) {
+    return dtype == LCI_BF16 && (a.hd == 64 || a.hd == 128) && a.bs % lci::q8r::kStrip == 0 &&
+           a.H_q / a.H_kv <= lci::q8r::kRows;
+}
+
+template <int HD, int NW, bool MODS>
+lci_status launch_attn_q8_rows(const lci::AttnQ8Args& a, long long pairs, int nsplit,
+                               cudaStream_t st) {
+    auto kern = lci::sparse_attn_q8_rows_kernel<HD, NW, MODS>;
+    const int blocks = a.mass ? (a.topk + nsplit - 1) / nsplit : 0;
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [&] {
+        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        (int)lci::q8r::smem_bytes<HD, NW>(lci::kMaxTopk));
+    });
+    if (attr_err != cudaSuccess)
+        return fail(LCI_ERR_CUDA, "sparse_attn_q8: %s", cudaGetErrorString(attr_err));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(pairs * nsplit));
+    cfg.blockDim = dim3(NW * 32);
+    cfg.dynamicSmemBytes = lci::q8r::smem_bytes<HD, NW>(blocks);
+    cfg.stream = st;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = (unsigned)nsplit;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = nsplit > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, nsplit);
+    if (e != cudaSuccess) return fail(LCI_ERR_CUDA, "sparse_attn_q8: %s", cudaGetErrorString(e));
+    return check_launch("sparse_attn_q8");
+}
+
+// Splits of a pair over a cluster, and warps per CTA.
+struct RowsShape {
+    int nsplit, warps;
+};
+RowsShape rows_q8_shape(const lci::AttnQ8Args& a, long long pairs) {
+    long long n = (2 * 148 + pairs - 1) / pairs;
+    n = std::min<long long>({n, (long long)lci::q8r::kMaxSplit, (long long)a.topk});
+    const int nsplit = (int)std::max<long long>(n, 1);
+    return {nsplit, pairs * nsplit <= 148 ? 8 : 4};
+}
+
+template <int HD, bool MODS>
+lci_status launch_rows(const lci::AttnQ8Args& a, long long pairs, cudaStream_t st) {
+    const RowsShape sh = rows_q8_shape(a, pairs);
+    return sh.warps == 8 ? launch_attn_q8_rows<HD, 8, MODS>(a, pairs, sh.nsplit, st)
+                         : launch_attn_q8_rows<HD, 4, MODS>(a, pairs, sh.nsplit, st);
+}
+
 template <int IPT>
 void launch_evict(const lci_block_table* t, int32_t batch, const int32_t* ctx_len,
                   const float* weight, int32_t budget, int32_t sink, int32_t recent,
@@ -1546,6 +1602,12 @@ lci_status lci_sparse_attn_q8(const void* q, lci_dtype dtype, int32_t batch, int
     a.lse = d_lse;
     a.mass = d_mass;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const long long pairs = (long long)batch * S * a.H_kv;
+    if (rows_q8_fits(a, dtype) && pairs < (1ll << 27)) {
+        const bool mods = a.cap > 0.f || a.slopes;
+        if (a.hd == 128) return mods ? launch_rows<128, true>(a, pairs, cs) : launch_rows<128, false>(a, pairs, cs);
+        return mods ? launch_rows<64, true>(a, pairs, cs) : launch_rows<64, false>(a, pairs, cs);
+    }
     return dtype == LCI_F32 ? launch_attn_q8_simt<float>(a, batch, cs)
                             : launch_attn_q8_simt<__nv_bfloat16>(a, batch, cs);
 }
