@@ -11,6 +11,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "ptx.cuh"
 #include "q8_cache.cuh"
 
 namespace lci {
@@ -96,6 +97,7 @@ __global__ void __launch_bounds__(kQ8SimtWarps * 32) sparse_attn_q8_simt_kernel(
     float* bm = sml + 2 * kQ8SimtWarps;            // [topk] max of each block
     float* br = bm + a.topk;                       // [topk] weight sum of each block
     float* bt = br + a.topk;                       // [topk] mass over the group's heads
+    pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x, g = blockIdx.y;
     const int G = a.H_q / a.H_kv, hd = a.hd, bs = a.bs;

@@ -5,14 +5,15 @@
 #include <cooperative_groups.h>
 
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace lci {
 
 namespace bwu {
 constexpr int kRange = 1024;   // blocks of a sequence one cluster accumulates
-constexpr int kMaxSplit = 8;   // CTAs of a cluster, each taking a share of the rows
-constexpr int kMaxWarps = 16;
-constexpr int kRowsAhead = 4;  // rows a warp loads before it adds them
+constexpr int kMaxSplit = 16;  // CTAs of a cluster, each taking a share of the rows
+constexpr int kMaxWarps = 32;
+constexpr int kRowsAhead = 8;  // rows a warp loads before it adds them
 constexpr size_t smem_bytes(int warps) { return (size_t)warps * kRange * 4 + kRange * 8; }
 }  // namespace bwu
 
@@ -34,6 +35,7 @@ __global__ void __launch_bounds__(bwu::kMaxWarps * 32) block_weight_update_kerne
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     double* total = reinterpret_cast<double*>(smem_raw);            // [kRange]
     float* hist = reinterpret_cast<float*>(smem_raw + kRange * 8);  // [warps][kRange]
+    pdl_wait();
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
     const int split = blockIdx.x, b = blockIdx.z;
     const int j0 = blockIdx.y * kRange;
@@ -75,6 +77,7 @@ __global__ void __launch_bounds__(bwu::kMaxWarps * 32) block_weight_update_kerne
     __syncthreads();
     for (int j = tid; j < width; j += nt) {
         double x = 0.0;
+#pragma unroll 8
         for (int w = 0; w < nw; ++w) x += (double)hist[w * kRange + j];
         total[j] = x;
     }
@@ -83,8 +86,12 @@ __global__ void __launch_bounds__(bwu::kMaxWarps * 32) block_weight_update_kerne
         cluster.sync();
         // each CTA of the cluster finishes a share of the blocks
         for (int j = split * nt + tid; j < width; j += nsplit * nt) {
-            double x = 0.0;
-            for (int c = 0; c < nsplit; ++c) x += cluster.map_shared_rank(total, c)[j];
+            double y[kMaxSplit], x = 0.0;
+#pragma unroll
+            for (int c = 0; c < kMaxSplit; ++c)
+                y[c] = c < nsplit ? cluster.map_shared_rank(total, c)[j] : 0.0;
+#pragma unroll
+            for (int c = 0; c < kMaxSplit; ++c) x += y[c];
             float* w = weight + (size_t)b * nb_max + j0 + j;
             *w = (float)((double)decay * (double)*w + x);
         }
@@ -126,24 +133,37 @@ __device__ __forceinline__ int cta_exclusive_sum(int v, int* scratch, int& total
     return before + incl - v;
 }
 
-// Eviction, one CTA per sequence, IPT consecutive blocks per thread in
-// registers: the m-th largest weight key among the blocks that are neither the
-// first `sink` nor the last `recent` is found by a four-way search on its bits
-// (16 counting rounds: one packed warp reduction and one barrier each, whatever
-// the distribution of the weights), ties go to the lower block, and two prefix
-// sums give every block its place: kept blocks, then freed ones, then the rest
-// of the row, each in order. All inputs are in registers before the first
-// write, so outputs may be the inputs.
+// Eviction, one CTA per sequence; thread t takes blocks t, t + threads, ...
+// (coalesced loads and nearly coalesced stores). The m-th largest weight key
+// among the blocks that are neither the first `sink` nor the last `recent` is
+// found digit by digit (11, 11 and 10 bits) with a histogram in shared memory;
+// a warp's lanes that share their first lane's digit count as one addition, so
+// that tied weights do not serialise. Ties go to the lower block, and ballots
+// with a prefix sum over the (row of blocks, warp) counts give every block its
+// place: kept blocks, then freed ones, then the rest of the row, each in order.
+// Every input is read before the first write, so outputs may be the inputs.
+// Bound by the latency of that chain.
 template <int IPT>
 __global__ void __launch_bounds__(1024) cache_evict_kernel(
     const int32_t* table, const int32_t* ctx_len, const float* weight, int nb_max, int bs,
     int budget, int sink, int recent, int32_t* table_out, int32_t* ctx_out, float* weight_out,
     int32_t* kept_ids, int32_t* freed) {
-    __shared__ uint32_t s_cnt[2][32];
+    constexpr int kBins = 2048;
+    __shared__ int s_hist[kBins];
+    __shared__ int s_pick[2];  // chosen bin, entries in larger bins
     __shared__ int s_scan[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+    __shared__ int s_base[IPT * 32];
+    pdl_wait();
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+    const uint32_t below = (1u << lane) - 1u;
     const int b = blockIdx.x;
     const size_t base = (size_t)b * nb_max;
+    uint32_t key[IPT];
+#pragma unroll
+    for (int i = 0; i < IPT; ++i) {
+        const int j = i * nt + tid;
+        key[i] = j < nb_max ? weight_key(weight[base + j]) : 0u;
+    }
     const int ctx = ctx_len[b];
     const long long want = ctx > 0 ? ((long long)ctx + bs - 1) / bs : 0;
     // a context longer than its table row is left as it is
@@ -151,22 +171,26 @@ __global__ void __launch_bounds__(1024) cache_evict_kernel(
     if (bad && tid == 0) raise_status(kStatusBadBlockId);
     const int n = (int)(bad ? 0 : want);
     const bool trim = n > budget;
-    int page[IPT];
-    float w[IPT];
-    uint32_t key[IPT];
-    const int j0 = tid * IPT;
+    // Exclusive prefix, in block order, of flags given as a bit per item:
+    // s_base[i * nw + warp] is the count before row i of this warp.
+    auto prefix = [&](uint32_t flags) -> int {
 #pragma unroll
-    for (int i = 0; i < IPT; ++i) {
-        const int j = j0 + i;
-        page[i] = j < nb_max ? table[base + j] : 0;
-        w[i] = j < nb_max ? weight[base + j] : 0.f;
-    }
+        for (int i = 0; i < IPT; ++i) {
+            const uint32_t v = __ballot_sync(0xffffffffu, (flags >> i) & 1u);
+            if (lane == 0) s_base[i * nw + warp] = __popc(v);
+        }
+        __syncthreads();
+        int total;
+        const int mine = cta_exclusive_sum(tid < IPT * nw ? s_base[tid] : 0, s_scan, total);
+        if (tid < IPT * nw) s_base[tid] = mine;
+        __syncthreads();
+        return total;
+    };
     // candidates: the middle blocks of a sequence that is trimmed
-    uint32_t cand = 0, keep = 0;
+    uint32_t cand = 0u, keep = 0u;
 #pragma unroll
     for (int i = 0; i < IPT; ++i) {
-        const int j = j0 + i;
-        key[i] = weight_key(w[i]);
+        const int j = i * nt + tid;
         if (j < n) {
             if (!trim || j < sink || j >= n - recent)
                 keep |= 1u << i;
@@ -177,65 +201,97 @@ __global__ void __launch_bounds__(1024) cache_evict_kernel(
     if (trim) {  // the same for every thread of the CTA
         const int m = budget - sink - recent;  // candidates to keep, fewer than there are
         if (m > 0) {
-            // t: the largest key value with at least m candidates at or above it
-            uint32_t t = 0u;
+            uint32_t t = 0u, known = 0u;  // digits found so far, and their bits
+            int need = m;                 // entries still to take among those that match t
 #pragma unroll 1
-            for (int bit = 30, round = 0; bit >= 0; bit -= 2, ++round) {
-                const uint32_t q1 = t | (1u << bit), q2 = t | (2u << bit), q3 = t | (3u << bit);
-                uint32_t c = 0u;
-#pragma unroll
-                for (int i = 0; i < IPT; ++i)
-                    if ((cand >> i) & 1u)
-                        c += (key[i] >= q1 ? 1u : 0u) + (key[i] >= q2 ? 1u << 10 : 0u) +
-                             (key[i] >= q3 ? 1u << 20 : 0u);
-                c = __reduce_add_sync(0xffffffffu, c);  // each count <= 32 * 16 < 2^10
-                if (lane == 0) s_cnt[round & 1][warp] = c;
+            for (int pass = 0; pass < 3; ++pass) {
+                const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+                const uint32_t digits = pass == 2 ? 1023u : 2047u;
+                for (int e = tid; e < kBins; e += nt) s_hist[e] = 0;
                 __syncthreads();
-                const uint32_t v = lane < nw ? s_cnt[round & 1][lane] : 0u;
-                const int c1 = __reduce_add_sync(0xffffffffu, v & 1023u);
-                const int c2 = __reduce_add_sync(0xffffffffu, (v >> 10) & 1023u);
-                const int c3 = __reduce_add_sync(0xffffffffu, v >> 20);
-                t = c3 >= m ? q3 : c2 >= m ? q2 : c1 >= m ? q1 : t;
+#pragma unroll
+                for (int i = 0; i < IPT; ++i) {
+                    const bool on = ((cand >> i) & 1u) && (key[i] & known) == t;
+                    const uint32_t act = __ballot_sync(0xffffffffu, on);
+                    if (act == 0u) continue;
+                    const uint32_t d = (key[i] >> shift) & digits;
+                    const int first = __ffs(act) - 1;
+                    const uint32_t d0 = __shfl_sync(0xffffffffu, d, first);
+                    const uint32_t same = __ballot_sync(0xffffffffu, on && d == d0);
+                    if (lane == first)
+                        atomicAdd(&s_hist[d0], __popc(same));
+                    else if (on && d != d0)
+                        atomicAdd(&s_hist[d], 1);
+                }
+                __syncthreads();
+                // the bin, from the largest down, in which the need-th entry lies
+                const int per = (kBins + nt - 1) / nt;
+                int sum = 0;
+                for (int e = 0; e < per; ++e) {
+                    const int r = tid * per + e;
+                    if (r < kBins) sum += s_hist[kBins - 1 - r];
+                }
+                int all;
+                int before = cta_exclusive_sum(sum, s_scan, all);
+                if (before < need && before + sum >= need) {  // one thread
+                    for (int e = 0; e < per; ++e) {
+                        const int c = s_hist[kBins - 1 - (tid * per + e)];
+                        if (before + c >= need) {
+                            s_pick[0] = kBins - 1 - (tid * per + e);
+                            s_pick[1] = before;
+                            break;
+                        }
+                        before += c;
+                    }
+                }
+                __syncthreads();
+                t |= (uint32_t)s_pick[0] << shift;
+                known |= digits << shift;
+                need -= s_pick[1];
             }
             uint32_t ties = 0u;
-            int above = 0;
 #pragma unroll
             for (int i = 0; i < IPT; ++i)
                 if ((cand >> i) & 1u) {
-                    if (key[i] > t) {
+                    if (key[i] > t)
                         keep |= 1u << i;
-                        ++above;
-                    } else if (key[i] == t) {
+                    else if (key[i] == t)
                         ties |= 1u << i;
-                    }
                 }
-            int n_above, n_ties;
-            cta_exclusive_sum(above, s_scan, n_above);
-            int left = m - n_above - cta_exclusive_sum(__popc(ties), s_scan, n_ties);
+            prefix(ties);
 #pragma unroll
-            for (int i = 0; i < IPT; ++i)
-                if ((ties >> i) & 1u) {
-                    if (left > 0) keep |= 1u << i;
-                    --left;
-                }
+            for (int i = 0; i < IPT; ++i) {
+                const uint32_t v = __ballot_sync(0xffffffffu, (ties >> i) & 1u);
+                if (((ties >> i) & 1u) && s_base[i * nw + warp] + __popc(v & below) < need)
+                    keep |= 1u << i;  // the lowest blocks first
+            }
+            __syncthreads();  // s_base is written again
         }
     }
-    int n_keep;
-    int pos = cta_exclusive_sum(__popc(keep), s_scan, n_keep);
+    int page[IPT];
+    float w[IPT];
+#pragma unroll
+    for (int i = 0; i < IPT; ++i) {  // read again (from L2): not held through the search
+        const int j = i * nt + tid;
+        page[i] = j < nb_max ? table[base + j] : 0;
+        w[i] = j < nb_max ? weight[base + j] : 0.f;
+    }
+    const int n_keep = prefix(keep);  // its barriers stand between the reads and the writes
 #pragma unroll
     for (int i = 0; i < IPT; ++i) {
-        const int j = j0 + i;
-        if (j >= nb_max) break;
+        const int j = i * nt + tid;
         const bool k = (keep >> i) & 1u;
-        // a freed block follows the kept ones, in order; others stay
-        const int to = j >= n ? j : k ? pos : n_keep + (j - pos);
-        table_out[base + to] = page[i];
-        weight_out[base + to] = k || bad ? w[i] : 0.f;
-        if (k && kept_ids && pos < budget) kept_ids[(size_t)b * budget + pos] = j;
-        pos += k ? 1 : 0;
+        const uint32_t v = __ballot_sync(0xffffffffu, k);
+        const int pos = s_base[i * nw + warp] + __popc(v & below);  // kept blocks before j
+        if (j < nb_max) {
+            const int to = j >= n ? j : k ? pos : n_keep + (j - pos);
+            table_out[base + to] = page[i];
+            weight_out[base + to] = k || bad ? w[i] : 0.f;
+            if (k && kept_ids && pos < budget) kept_ids[(size_t)b * budget + pos] = j;
+        }
     }
     if (kept_ids)
-        for (int i = n_keep + tid; i < budget; i += blockDim.x) kept_ids[(size_t)b * budget + i] = -1;
+        for (int i = n_keep + tid; i < budget; i += nt) kept_ids[(size_t)b * budget + i] = -1;
     if (tid == 0) {
         const int gone = n - n_keep;
         ctx_out[b] = ctx - gone * bs;

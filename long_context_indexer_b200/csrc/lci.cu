@@ -1417,16 +1417,42 @@ lci_status check_q8_table(const char* what, const lci_block_table* t, int32_t ba
     return LCI_OK;
 }
 
+// A launch that may be scheduled under the tail of the previous kernel of the
+// stream; the kernel itself waits for that kernel before it reads or writes.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_early(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                         cudaStream_t st, int cluster, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = (unsigned)cluster;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cfg.attrs = attrs;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
 template <typename T, int VEC>
-void launch_kv_append(const void* k_new, const void* v_new, int32_t batch, int32_t T_new,
-                      const int32_t* start, const int32_t* count, const lci_block_table* t,
-                      void* k_pool, void* v_pool, float* k_scale, float* v_scale, int slots,
-                      cudaStream_t st) {
-    const dim3 grid((unsigned)((long long)batch * slots * t->num_kv_heads), 2);
-    lci::kv_append_q8_kernel<T, VEC><<<grid, 256, 0, st>>>(
-        static_cast<const T*>(k_new), static_cast<const T*>(v_new), batch, T_new, t->num_kv_heads,
-        t->head_dim, t->block_size, start, count, t->d_table, t->max_blocks, t->num_pages, slots,
-        static_cast<uint8_t*>(k_pool), static_cast<uint8_t*>(v_pool), k_scale, v_scale);
+cudaError_t launch_kv_append(const void* k_new, const void* v_new, int32_t batch, int32_t T_new,
+                             const int32_t* start, const int32_t* count, const lci_block_table* t,
+                             void* k_pool, void* v_pool, float* k_scale, float* v_scale, int slots,
+                             cudaStream_t st) {
+    // two runs of K and of V per thread cover a block
+    const long long runs = (long long)std::min(T_new, t->block_size) * (t->head_dim / VEC);
+    const long long want = ((runs + lci::kAppendHold - 1) / lci::kAppendHold + 31) / 32 * 32;
+    const int threads = (int)std::min<long long>(std::max<long long>(want, 128), lci::kAppendMaxThreads);
+    return launch_early(lci::kv_append_q8_kernel<T, VEC>,
+                        dim3((unsigned)((long long)batch * slots * t->num_kv_heads)), dim3(threads), 0,
+                        st, 1, static_cast<const T*>(k_new), static_cast<const T*>(v_new), T_new,
+                        t->num_kv_heads, t->head_dim, t->block_size, start, count, t->d_table,
+                        t->max_blocks, t->num_pages, slots, static_cast<uint8_t*>(k_pool),
+                        static_cast<uint8_t*>(v_pool), k_scale, v_scale);
 }
 
 template <typename T>
@@ -1434,7 +1460,9 @@ lci_status launch_attn_q8_simt(const lci::AttnQ8Args& a, int32_t batch, cudaStre
     const size_t smem = (size_t)(a.hd * (1 + lci::kQ8SimtWarps) + 2 * lci::kQ8SimtWarps +
                                  3 * a.topk) * 4;
     const dim3 grid((unsigned)(batch * a.S), (unsigned)a.H_kv);
-    lci::sparse_attn_q8_simt_kernel<T><<<grid, lci::kQ8SimtWarps * 32, smem, st>>>(a);
+    const cudaError_t e = launch_early(lci::sparse_attn_q8_simt_kernel<T>, grid,
+                                       dim3(lci::kQ8SimtWarps * 32), smem, st, 1, a);
+    if (e != cudaSuccess) return fail(LCI_ERR_CUDA, "sparse_attn_q8: %s", cudaGetErrorString(e));
     return check_launch("sparse_attn_q8");
 }
 
@@ -1457,20 +1485,8 @@ lci_status launch_attn_q8_rows(const lci::AttnQ8Args& a, long long pairs, int ns
     });
     if (attr_err != cudaSuccess)
         return fail(LCI_ERR_CUDA, "sparse_attn_q8: %s", cudaGetErrorString(attr_err));
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(pairs * nsplit));
-    cfg.blockDim = dim3(NW * 32);
-    cfg.dynamicSmemBytes = lci::q8r::smem_bytes<HD, NW>(blocks);
-    cfg.stream = st;
-    cudaLaunchAttribute attrs[2];
-    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attrs[0].val.programmaticStreamSerializationAllowed = 1;
-    attrs[1].id = cudaLaunchAttributeClusterDimension;
-    attrs[1].val.clusterDim.x = (unsigned)nsplit;
-    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
-    cfg.attrs = attrs;
-    cfg.numAttrs = nsplit > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, nsplit);
+    const cudaError_t e = launch_early(kern, dim3((unsigned)(pairs * nsplit)), dim3(NW * 32),
+                                       lci::q8r::smem_bytes<HD, NW>(blocks), st, nsplit, a, nsplit);
     if (e != cudaSuccess) return fail(LCI_ERR_CUDA, "sparse_attn_q8: %s", cudaGetErrorString(e));
     return check_launch("sparse_attn_q8");
 }
@@ -1494,14 +1510,14 @@ lci_status launch_rows(const lci::AttnQ8Args& a, long long pairs, cudaStream_t s
 }
 
 template <int IPT>
-void launch_evict(const lci_block_table* t, int32_t batch, const int32_t* ctx_len,
-                  const float* weight, int32_t budget, int32_t sink, int32_t recent,
-                  int32_t* table_out, int32_t* ctx_out, float* weight_out, int32_t* kept,
-                  int32_t* freed, cudaStream_t st) {
+cudaError_t launch_evict(const lci_block_table* t, int32_t batch, const int32_t* ctx_len,
+                         const float* weight, int32_t budget, int32_t sink, int32_t recent,
+                         int32_t* table_out, int32_t* ctx_out, float* weight_out, int32_t* kept,
+                         int32_t* freed, cudaStream_t st) {
     const int threads = ((t->max_blocks + IPT - 1) / IPT + 31) / 32 * 32;
-    lci::cache_evict_kernel<IPT><<<(unsigned)batch, threads, 0, st>>>(
-        t->d_table, ctx_len, weight, t->max_blocks, t->block_size, budget, sink, recent, table_out,
-        ctx_out, weight_out, kept, freed);
+    return launch_early(lci::cache_evict_kernel<IPT>, dim3((unsigned)batch), dim3(threads), 0, st, 1,
+                        t->d_table, ctx_len, weight, t->max_blocks, t->block_size, budget, sink,
+                        recent, table_out, ctx_out, weight_out, kept, freed);
 }
 
 }  // namespace
@@ -1531,7 +1547,9 @@ lci_status lci_kv_append_q8(const void* k_new, const void* v_new, lci_dtype dtyp
     auto run = dtype == LCI_F32 ? (vec ? launch_kv_append<float, 16> : launch_kv_append<float, 1>)
                                 : (vec ? launch_kv_append<__nv_bfloat16, 16>
                                        : launch_kv_append<__nv_bfloat16, 1>);
-    run(k_new, v_new, batch, T, d_start, d_count, table, k_pool, v_pool, k_scale, v_scale, slots, cs);
+    const cudaError_t e = run(k_new, v_new, batch, T, d_start, d_count, table, k_pool, v_pool,
+                              k_scale, v_scale, slots, cs);
+    if (e != cudaSuccess) return fail(LCI_ERR_CUDA, "kv_append_q8: %s", cudaGetErrorString(e));
     return check_launch("kv_append_q8");
 }
 
@@ -1630,29 +1648,25 @@ lci_status lci_block_weight_update(const int32_t* d_ids, const float* d_mass, in
         attr_err = cudaFuncSetAttribute(lci::block_weight_update_kernel,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (int)lci::bwu::smem_bytes(lci::bwu::kMaxWarps));
+        if (attr_err == cudaSuccess)  // clusters of 16
+            attr_err = cudaFuncSetAttribute(lci::block_weight_update_kernel,
+                                            cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     });
     if (attr_err != cudaSuccess)
         return fail(LCI_ERR_CUDA, "block_weight_update: %s", cudaGetErrorString(attr_err));
-    // a few rows per warp: up to 16 warps, then up to 8 CTAs
+    // Rows are spread over warps, then over the CTAs of a cluster (while the
+    // grid has room), until a warp has the few rows it loads at once.
     const int ranges = (max_blocks + lci::bwu::kRange - 1) / lci::bwu::kRange;
-    int nsplit = 1;
-    while (nsplit < lci::bwu::kMaxSplit &&
-           S > nsplit * lci::bwu::kMaxWarps * lci::bwu::kRowsAhead) nsplit *= 2;
     int warps = 4;
-    while (warps < lci::bwu::kMaxWarps && S > nsplit * warps * lci::bwu::kRowsAhead) warps *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)nsplit, (unsigned)ranges, (unsigned)batch);
-    cfg.blockDim = dim3((unsigned)warps * 32);
-    cfg.dynamicSmemBytes = lci::bwu::smem_bytes(warps);
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)nsplit;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = nsplit > 1 ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, lci::block_weight_update_kernel, d_ids, d_mass, S,
-                                             num_kv_heads, topk, max_blocks, decay, d_weight, nsplit);
+    while (warps < lci::bwu::kMaxWarps && S > warps * lci::bwu::kRowsAhead) warps *= 2;
+    int nsplit = 1;
+    while (nsplit < lci::bwu::kMaxSplit && S > nsplit * warps * lci::bwu::kRowsAhead &&
+           2ll * nsplit * ranges * batch <= 148)
+        nsplit *= 2;
+    const cudaError_t e = launch_early(
+        lci::block_weight_update_kernel, dim3((unsigned)nsplit, (unsigned)ranges, (unsigned)batch),
+        dim3((unsigned)warps * 32), lci::bwu::smem_bytes(warps), static_cast<cudaStream_t>(stream),
+        nsplit, d_ids, d_mass, S, num_kv_heads, topk, max_blocks, decay, d_weight, nsplit);
     if (e != cudaSuccess) return fail(LCI_ERR_CUDA, "block_weight_update: %s", cudaGetErrorString(e));
     return check_launch("block_weight_update");
 }
@@ -1676,8 +1690,9 @@ lci_status lci_cache_evict(const lci_block_table* table, int32_t batch, const in
     // blocks per thread: up to 1024 threads
     const int nb = table->max_blocks;
     auto run = nb <= 1024 ? launch_evict<1> : nb <= 4096 ? launch_evict<4> : launch_evict<16>;
-    run(table, batch, d_ctx_len, d_weight, budget, sink, recent, d_table_out, d_ctx_out,
-        d_weight_out, d_kept, d_freed, cs);
+    const cudaError_t e = run(table, batch, d_ctx_len, d_weight, budget, sink, recent, d_table_out,
+                              d_ctx_out, d_weight_out, d_kept, d_freed, cs);
+    if (e != cudaSuccess) return fail(LCI_ERR_CUDA, "cache_evict: %s", cudaGetErrorString(e));
     return check_launch("cache_evict");
 }
 

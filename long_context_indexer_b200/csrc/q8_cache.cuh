@@ -13,6 +13,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace lci {
 
@@ -60,33 +61,89 @@ __device__ __forceinline__ float e4m3_scale(float amax) {
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-__device__ __forceinline__ void load_run(const float* p, float (&x)[16]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
-        x[4 * i] = v.x;
-        x[4 * i + 1] = v.y;
-        x[4 * i + 2] = v.z;
-        x[4 * i + 3] = v.w;
+// VEC consecutive new elements as loaded.
+template <typename T, int VEC> struct RawRun;
+// Largest finite magnitude of elements seen.
+struct AmaxF32 {
+    float m = 0.f;
+    __device__ __forceinline__ void add(float x) {
+        const float a = fabsf(x);
+        m = a <= 3.402823466e38f ? fmaxf(m, a) : m;
     }
-}
-__device__ __forceinline__ void load_run(const __nv_bfloat16* p, float (&x)[16]) {
+};
+template <> struct RawRun<float, 16> {
+    float4 w[4];
+    __device__ __forceinline__ void fold(AmaxF32& a) const {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = bf16x2_to_f32(w[j]);
-            x[8 * i + 2 * j] = f.x;
-            x[8 * i + 2 * j + 1] = f.y;
+        for (int i = 0; i < 4; ++i) {
+            a.add(w[i].x);
+            a.add(w[i].y);
+            a.add(w[i].z);
+            a.add(w[i].w);
         }
     }
-}
-template <typename T>
-__device__ __forceinline__ void load_run(const T* p, float (&x)[1]) {
-    x[0] = to_f32(*p);
-}
+    __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
+    }
+    __device__ __forceinline__ void get(float (&x)[16]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[4 * i] = w[i].x;
+            x[4 * i + 1] = w[i].y;
+            x[4 * i + 2] = w[i].z;
+            x[4 * i + 3] = w[i].w;
+        }
+    }
+};
+template <> struct RawRun<__nv_bfloat16, 16> {
+    uint4 w[2];
+    // Packed maxima of magnitudes (the maximum drops NaN); infinities, which
+    // do not count, are rare and taken out of the pair that holds one.
+    __device__ __forceinline__ void fold(AmaxF32& a) const {
+        __nv_bfloat162 m = __float2bfloat162_rn(0.f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&u[j])));
+        }
+        const float2 f = __bfloat1622float2(m);
+        const float x = fmaxf(f.x, f.y);
+        if (x <= 3.402823466e38f) {
+            a.m = fmaxf(a.m, x);
+        } else {
+            float y[16];
+            get(y);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) a.add(y[i]);
+        }
+    }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    }
+    __device__ __forceinline__ void get(float (&x)[16]) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = bf16x2_to_f32(u[j]);
+                x[8 * i + 2 * j] = f.x;
+                x[8 * i + 2 * j + 1] = f.y;
+            }
+        }
+    }
+};
+template <typename T> struct RawRun<T, 1> {
+    T w;
+    __device__ __forceinline__ void fold(AmaxF32& a) const { a.add(to_f32(w)); }
+    __device__ __forceinline__ void load(const T* p) { w = *p; }
+    __device__ __forceinline__ void get(float (&x)[1]) const { x[0] = to_f32(w); }
+};
+
 __device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[16]) {
     uint4 v;
     v.x = f32_to_e4m3x4(x[0], x[1], x[2], x[3]);
@@ -98,131 +155,150 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[16]) {
 __device__ __forceinline__ void store_codes(uint8_t* p, const float (&x)[1]) {
     *p = (uint8_t)f32_to_e4m3x2(x[0], 0.f);
 }
+__device__ __forceinline__ void load_codes(const uint8_t* p, float (&x)[16]) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        float f[4];
+        e4m3x4_to_f32(w[q], f);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[4 * q + r] = f[r];
+    }
+}
+__device__ __forceinline__ void load_codes(const uint8_t* p, float (&x)[1]) { x[0] = e4m3_to_f32(*p); }
 
-// One CTA per (touched block, KV head, K or V). It owns that head of the page:
-// the largest finite magnitude of the new tokens gives the scale they need, the
-// page keeps the larger of that and its own scale if it already held tokens,
-// stored codes are rounded to a scale that grew, and the new tokens' codes are
-// written. A thread's first kHold runs of new elements stay in registers
-// between the two passes; further ones are read again (from L2).
-// Slots behind the last token are not touched.
+constexpr int kAppendMaxThreads = 256;
+constexpr int kAppendHold = 2;  // runs of new K, and of new V, a thread holds
+
+// One CTA per (touched block, KV head), for K and V. It owns that head of the
+// page: the largest finite magnitude of the new tokens gives the scale they
+// need, the page keeps the larger of that and its own scale if it already held
+// tokens, stored codes are rounded to a scale that grew, and the new tokens'
+// codes are written. New elements stay in registers, as loaded, between the
+// two passes (a thread's first kAppendHold runs; further ones, only in blocks
+// of more than 8192 elements, are read again from L2). Slots behind the last
+// token are not touched.
+//
+// Bound by HBM for a prompt: K and V of a cell are loaded together so that a
+// CTA has 32 KiB in flight behind one chain of lookups, and holding raw bf16
+// instead of floats keeps four CTAs on an SM.
 template <typename T, int VEC>
-__global__ void __launch_bounds__(256) kv_append_q8_kernel(
-    const T* __restrict__ k_new, const T* __restrict__ v_new, int batch, int T_new, int H_kv, int hd,
-    int bs, const int32_t* __restrict__ start, const int32_t* __restrict__ count,
+__global__ void __launch_bounds__(kAppendMaxThreads, sizeof(T) == 2 ? 4 : 2) kv_append_q8_kernel(
+    const T* __restrict__ k_new, const T* __restrict__ v_new, int T_new, int H_kv, int hd, int bs,
+    const int32_t* __restrict__ start, const int32_t* __restrict__ count,
     const int32_t* __restrict__ table, int nb_max, int num_pages, int slots, uint8_t* k_pool,
     uint8_t* v_pool, float* k_scale, float* v_scale) {
-    constexpr int kHold = VEC == 16 ? 2 : 16;
-    __shared__ float s_amax[8];
+    __shared__ float s_amax[2][kAppendMaxThreads / 32];
+    pdl_wait();
     const unsigned tid = threadIdx.x, nt = blockDim.x;
     const int g = blockIdx.x % H_kv;
-    const bool is_v = blockIdx.y != 0;
     const int bslot = blockIdx.x / H_kv;
     const int b = bslot / slots, slot = bslot - b * slots;
     const long long p0 = start[b];
     const int n_new = count ? min(max(count[b], 0), T_new) : T_new;
     if (n_new == 0) return;
+    if (p0 < 0) {
+        if (tid == 0) raise_status(kStatusBadBlockId);
+        return;
+    }
     const long long j = p0 / bs + slot;
     const long long t_lo = slot == 0 ? p0 : j * bs;                 // first new token of this block
     const long long t_hi = min(p0 + n_new, (j + 1) * (long long)bs);  // past its last one
-    if (p0 < 0 || t_lo >= t_hi) {
-        if (p0 < 0 && tid == 0) raise_status(kStatusBadBlockId);
-        return;
-    }
+    if (t_lo >= t_hi) return;
     if (j >= nb_max) {
         if (tid == 0) raise_status(kStatusBadBlockId);
         return;
     }
+    // the new elements do not wait for the page: both loads are in flight together
     const int page = table[(size_t)b * nb_max + j];
+    const int held = (int)(t_lo - j * bs);  // tokens the block already holds
+    const unsigned runs = hd / VEC;
+    const unsigned total = (unsigned)(t_hi - t_lo) * runs;  // below 2^31 (block_size * head_dim)
+    const size_t src0 = (((size_t)b * T_new + (size_t)(t_lo - p0)) * H_kv + g) * hd;
+    const size_t tok_stride = (size_t)H_kv * hd;
+    auto src = [&](unsigned e) { return src0 + (size_t)(e / runs) * tok_stride + (size_t)(e % runs) * VEC; };
+
+    RawRun<T, VEC> x[2][kAppendHold];
+#pragma unroll
+    for (int i = 0; i < kAppendHold; ++i) {
+        const unsigned e = tid + i * nt;
+        if (e < total) {
+            const size_t at = src(e);
+            x[0][i].load(k_new + at);
+            x[1][i].load(v_new + at);
+        }
+    }
     if (page < 0 || page >= num_pages) {
         if (tid == 0) raise_status(kStatusBadPage);
         return;
     }
-    const int held = (int)(t_lo - j * bs);  // tokens the block already holds
-    const unsigned runs = hd / VEC;
-    const unsigned total = (unsigned)(t_hi - t_lo) * runs;  // below 2^31 (block_size * head_dim)
-    const T* src = (is_v ? v_new : k_new) + (((size_t)b * T_new + (size_t)(t_lo - p0)) * H_kv + g) * hd;
-    const size_t tok_stride = (size_t)H_kv * hd;
     const size_t cell = (size_t)page * H_kv + g;
-    uint8_t* dst = (is_v ? v_pool : k_pool) + cell * bs * hd;
-    float* sc = (is_v ? v_scale : k_scale) + cell;
-    const float s_old = held > 0 ? *sc : 0.f;
-
-    float x[kHold][VEC];
-    float amax = 0.f;
-    auto fold = [&](const float (&y)[VEC]) {
+    const float s_old[2] = {held > 0 ? k_scale[cell] : 0.f, held > 0 ? v_scale[cell] : 0.f};
+    AmaxF32 seen[2];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const float a = fabsf(y[e]);
-            amax = a <= 3.402823466e38f ? fmaxf(amax, a) : amax;  // finite values only
+    for (int i = 0; i < kAppendHold; ++i)
+        if (tid + i * nt < total) {
+            x[0][i].fold(seen[0]);
+            x[1][i].fold(seen[1]);
         }
-    };
-#pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-        const unsigned e = tid + i * nt;
-        if (e < total) load_run(src + (size_t)(e / runs) * tok_stride + (size_t)(e % runs) * VEC, x[i]);
+    for (unsigned e = tid + kAppendHold * nt; e < total; e += nt) {
+        RawRun<T, VEC> y;
+        y.load(k_new + src(e));
+        y.fold(seen[0]);
+        y.load(v_new + src(e));
+        y.fold(seen[1]);
     }
+    float amax[2] = {seen[0].m, seen[1].m};
 #pragma unroll
-    for (int i = 0; i < kHold; ++i)
-        if (tid + i * nt < total) fold(x[i]);
-    for (unsigned e = tid + kHold * nt; e < total; e += nt) {
-        float y[VEC];
-        load_run(src + (size_t)(e / runs) * tok_stride + (size_t)(e % runs) * VEC, y);
-        fold(y);
+    for (int kv = 0; kv < 2; ++kv) {
+        amax[kv] = warp_max(amax[kv]);
+        if ((tid & 31) == 0) s_amax[kv][tid >> 5] = amax[kv];
     }
-    amax = warp_max(amax);
-    if ((tid & 31) == 0) s_amax[tid >> 5] = amax;
     __syncthreads();
-    for (unsigned w = 0; w < (nt >> 5); ++w) amax = fmaxf(amax, s_amax[w]);
-    const float s_new = fmaxf(s_old, e4m3_scale(amax));
-    // a power of two is divided by exactly with its reciprocal; a scale from
-    // elsewhere takes the division
-    const bool pow2 = (__float_as_uint(s_new) & 0x7fffffu) == 0u;
-    const float inv = 1.f / s_new;
-    auto put = [&](uint8_t* p, float (&y)[VEC]) {
-        if (pow2) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) y[e] *= inv;
-        } else {
+    for (int kv = 0; kv < 2; ++kv) {
+        amax[kv] = warp_max((tid & 31) < (nt >> 5) ? s_amax[kv][tid & 31] : 0.f);
+        const float s_new = fmaxf(s_old[kv], e4m3_scale(amax[kv]));
+        uint8_t* dst = (kv ? v_pool : k_pool) + cell * bs * hd;
+        // a power of two is divided by exactly with its reciprocal; a scale
+        // from elsewhere takes the division
+        const bool pow2 = (__float_as_uint(s_new) & 0x7fffffu) == 0u;
+        const float inv = 1.f / s_new;
+        auto put = [&](uint8_t* p, const RawRun<T, VEC>& r) {
+            float y[VEC];
+            r.get(y);
+            if (pow2) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) y[e] = y[e] / s_new;
-        }
-        store_codes(p, y);
-    };
-    if (tid == 0) *sc = s_new;  // every thread has read s_old before the barrier
-    if (held > 0 && s_new > s_old) {
-        const float ratio = s_old / s_new;
-        const unsigned old_runs = (unsigned)held * runs;
-        for (unsigned e = tid; e < old_runs; e += nt) {
-            uint8_t* p = dst + (size_t)e * VEC;
-            if constexpr (VEC == 16) {
-                const uint4 v = *reinterpret_cast<const uint4*>(p);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                float y[16];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float f[4];
-                    e4m3x4_to_f32(w[q], f);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) y[4 * q + r] = f[r] * ratio;
-                }
-                store_codes(p, y);
+                for (int e = 0; e < VEC; ++e) y[e] *= inv;
             } else {
-                float y[1] = {e4m3_to_f32(*p) * ratio};
-                store_codes(p, y);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) y[e] = y[e] / s_new;
+            }
+            store_codes(p, y);
+        };
+        if (tid == 0) (kv ? v_scale : k_scale)[cell] = s_new;  // all have read s_old: the barrier
+        if (held > 0 && s_new > s_old[kv]) {
+            const float ratio = s_old[kv] / s_new;
+            for (unsigned e = tid; e < (unsigned)held * runs; e += nt) {
+                float y[VEC];
+                load_codes(dst + (size_t)e * VEC, y);
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) y[q] *= ratio;
+                store_codes(dst + (size_t)e * VEC, y);
             }
         }
-    }
-    uint8_t* fresh = dst + (size_t)held * hd;
+        uint8_t* fresh = dst + (size_t)held * hd;
 #pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-        const unsigned e = tid + i * nt;
-        if (e < total) put(fresh + (size_t)e * VEC, x[i]);
-    }
-    for (unsigned e = tid + kHold * nt; e < total; e += nt) {
-        float y[VEC];
-        load_run(src + (size_t)(e / runs) * tok_stride + (size_t)(e % runs) * VEC, y);
-        put(fresh + (size_t)e * VEC, y);
+        for (int i = 0; i < kAppendHold; ++i) {
+            const unsigned e = tid + i * nt;
+            if (e < total) put(fresh + (size_t)e * VEC, x[kv][i]);
+        }
+        for (unsigned e = tid + kAppendHold * nt; e < total; e += nt) {
+            RawRun<T, VEC> y;
+            y.load((kv ? v_new : k_new) + src(e));
+            put(fresh + (size_t)e * VEC, y);
+        }
     }
 }
 

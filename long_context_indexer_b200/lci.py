@@ -534,6 +534,11 @@ class _ScoreOptions(ctypes.Structure):
     _fields_ = [("cap", _f32), ("d_slopes", _vp), ("d_first", _vp), ("d_last", _vp)]
 
 
+# The handle of a device's current stream, without building a stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 class PreparedCall:
     """A checked call of one entry point, for a loop that makes it every step:
     the tensors were checked and their pointers taken when it was prepared, and
@@ -548,7 +553,7 @@ class PreparedCall:
         self._device = device.index
 
     def __call__(self, stream=None):
-        raw = (torch.cuda.current_stream(self._device) if stream is None else stream).cuda_stream
+        raw = _raw_stream(self._device) if stream is None else stream.cuda_stream
         if torch.cuda.current_device() == self._device:
             rc = self._fn(*self._args, raw)
         else:
