@@ -44,32 +44,33 @@ __global__ void __launch_bounds__(bwu::kMaxWarps * 32) block_weight_update_kerne
     for (int j = lane; j < width; j += 32) mine[j] = 0.f;
     __syncwarp();
     const int stride = nsplit * nw;
+    const size_t step = (size_t)stride * topk;  // entries between two rows of this warp
     for (int s0 = split * nw + warp; s0 < S; s0 += stride * kRowsAhead) {
-        for (int i0 = 0; i0 < topk; i0 += 32) {
-            const int i = i0 + lane;
+        for (int i = lane; i < ((topk + 31) & ~31); i += 32) {
+            const size_t at = ((size_t)b * S + s0) * topk + i;
+            const int32_t* idp = ids + at;
+            const float* mp = mass + (((size_t)b * S + s0) * H_kv * topk + i);
+            const int rows = i < topk ? min(kRowsAhead, (S - s0 + stride - 1) / stride) : 0;
             int id[kRowsAhead];
             float add[kRowsAhead];
 #pragma unroll
             for (int k = 0; k < kRowsAhead; ++k) {
-                const int s = s0 + k * stride;
-                id[k] = -1;
-                add[k] = 0.f;
-                if (s < S && i < topk) {
-                    id[k] = ids[((size_t)b * S + s) * topk + i];
-                    const float* m = mass + ((size_t)b * S + s) * H_kv * topk + i;
-                    float x = 0.f;
-                    for (int g = 0; g < H_kv; ++g) x += m[(size_t)g * topk];
-                    add[k] = x;
-                }
+                id[k] = k < rows ? __ldg(idp + k * step) : -1;
+                add[k] = k < rows ? __ldg(mp + k * step * H_kv) : 0.f;
+            }
+            for (int g = 1; g < H_kv; ++g) {
+                mp += topk;
+#pragma unroll
+                for (int k = 0; k < kRowsAhead; ++k)
+                    add[k] += k < rows ? __ldg(mp + k * step * H_kv) : 0.f;
             }
 #pragma unroll
             for (int k = 0; k < kRowsAhead; ++k) {
-                const int j = id[k];
-                if (j < -1 || j >= nb_max) {
-                    if (blockIdx.y == 0) raise_status(kStatusBadBlockId);
-                } else if (j >= j0 && j < j0 + width) {
-                    mine[j - j0] += add[k];
-                }
+                const unsigned at_j = (unsigned)(id[k] - j0);
+                if (at_j < (unsigned)width)
+                    mine[at_j] += add[k];
+                else if ((unsigned)(id[k] + 1) > (unsigned)nb_max)
+                    raise_status(kStatusBadBlockId);
                 __syncwarp();
             }
         }
@@ -110,6 +111,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 // Exclusive prefix sum of one int per thread over the CTA (up to 32 warps).
+// scratch[32] must not be written again before the CTA's next barrier.
 __device__ __forceinline__ int cta_exclusive_sum(int v, int* scratch, int& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     int incl = v;
@@ -120,77 +122,93 @@ __device__ __forceinline__ int cta_exclusive_sum(int v, int* scratch, int& total
     }
     if (lane == 31) scratch[warp] = incl;
     __syncthreads();
-    int ws = lane < nw ? scratch[lane] : 0;
-    int wi = ws;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, wi, o);
-        if (lane >= o) wi += t;
-    }
-    total = __shfl_sync(0xffffffffu, wi, 31);
-    const int before = __shfl_sync(0xffffffffu, wi - ws, warp);
-    __syncthreads();  // scratch may be used again
+    const int ws = lane < nw ? scratch[lane] : 0;
+    total = __reduce_add_sync(0xffffffffu, ws);
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0);
     return before + incl - v;
 }
 
-// Eviction, one CTA per sequence; thread t takes blocks t, t + threads, ...
-// (coalesced loads and nearly coalesced stores). The m-th largest weight key
-// among the blocks that are neither the first `sink` nor the last `recent` is
-// found digit by digit (11, 11 and 10 bits) with a histogram in shared memory;
-// a warp's lanes that share their first lane's digit count as one addition, so
-// that tied weights do not serialise. Ties go to the lower block, and ballots
-// with a prefix sum over the (row of blocks, warp) counts give every block its
-// place: kept blocks, then freed ones, then the rest of the row, each in order.
-// Every input is read before the first write, so outputs may be the inputs.
-// Bound by the latency of that chain.
+// Eviction, one cluster of 1 to 8 CTAs per sequence, each CTA IPT * threads
+// consecutive blocks, thread t of it blocks t, t + threads, ... (coalesced loads
+// and nearly coalesced stores). The m-th largest weight key among the blocks
+// that are neither the first `sink` nor the last `recent` is found digit by
+// digit (11, 11 and 10 bits): every CTA counts its blocks in a histogram in
+// shared memory and adds its bins that are not empty to every CTA's sum
+// (distributed shared memory). A warp's lanes that share their first lane's
+// digit count as one addition, so that tied weights do not serialise, and the
+// search ends as soon as a whole bin is kept. Ties go to the lower block,
+// and ballots with a prefix sum over the (CTA, row of blocks, warp) counts give
+// every block its place: kept blocks, then freed ones, then the rest of the row,
+// each in order. Every input is read before a barrier of the cluster that
+// precedes the first write, so outputs may be the inputs. Bound by the latency
+// of that chain (five cluster barriers); one CTA for all 16384 blocks of a
+// sequence was bound by its instructions (28 us against 9).
 template <int IPT>
 __global__ void __launch_bounds__(1024) cache_evict_kernel(
     const int32_t* table, const int32_t* ctx_len, const float* weight, int nb_max, int bs,
     int budget, int sink, int recent, int32_t* table_out, int32_t* ctx_out, float* weight_out,
-    int32_t* kept_ids, int32_t* freed) {
+    int32_t* kept_ids, int32_t* freed, int nsplit) {
+    namespace cg = cooperative_groups;
     constexpr int kBins = 2048;
-    __shared__ int s_hist[kBins];
-    __shared__ int s_pick[2];  // chosen bin, entries in larger bins
-    __shared__ int s_scan[32];
-    __shared__ int s_base[IPT * 32];
+    __shared__ int s_own[kBins];     // this CTA's counts of one digit
+    __shared__ int s_sum[3][kBins];  // the cluster's, one array per digit
+    __shared__ int s_pick[3];        // chosen bin, entries in larger bins, entries in it
+    __shared__ int s_scan[2][32];
+    __shared__ int s_base[2][IPT * 32];
+    __shared__ int s_total[2];       // this CTA's ties and kept blocks
     pdl_wait();
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
     const uint32_t below = (1u << lane) - 1u;
-    const int b = blockIdx.x;
-    const size_t base = (size_t)b * nb_max;
-    uint32_t key[IPT];
+    const int split = blockIdx.x % nsplit, b = blockIdx.x / nsplit;
+    const int32_t* trow = table + (size_t)b * nb_max;
+    const float* wrow = weight + (size_t)b * nb_max;
+    const int jt = split * IPT * nt + tid;  // this thread's first block
+    int page[IPT];
+    float w[IPT];
 #pragma unroll
     for (int i = 0; i < IPT; ++i) {
-        const int j = i * nt + tid;
-        key[i] = j < nb_max ? weight_key(weight[base + j]) : 0u;
+        const int j = jt + i * nt;
+        w[i] = j < nb_max ? wrow[j] : 0.f;
+        page[i] = j < nb_max ? trow[j] : 0;
     }
     const int ctx = ctx_len[b];
     const long long want = ctx > 0 ? ((long long)ctx + bs - 1) / bs : 0;
     // a context longer than its table row is left as it is
     const bool bad = want > nb_max;
-    if (bad && tid == 0) raise_status(kStatusBadBlockId);
+    if (bad && split == 0 && tid == 0) raise_status(kStatusBadBlockId);
     const int n = (int)(bad ? 0 : want);
     const bool trim = n > budget;
+    auto cluster_sync = [&]() {
+        if (nsplit > 1)
+            cg::this_cluster().sync();
+        else
+            __syncthreads();
+    };
     // Exclusive prefix, in block order, of flags given as a bit per item:
-    // s_base[i * nw + warp] is the count before row i of this warp.
-    auto prefix = [&](uint32_t flags) -> int {
+    // s_base[which][i * nw + warp] is the count before row i of this warp in
+    // this CTA; returns the count in lower CTAs, all gets the cluster's total.
+    auto prefix = [&](uint32_t flags, int which, int& all) -> int {
+        int* at = s_base[which];
 #pragma unroll
         for (int i = 0; i < IPT; ++i) {
             const uint32_t v = __ballot_sync(0xffffffffu, (flags >> i) & 1u);
-            if (lane == 0) s_base[i * nw + warp] = __popc(v);
+            if (lane == 0) at[i * nw + warp] = __popc(v);
         }
         __syncthreads();
-        int total;
-        const int mine = cta_exclusive_sum(tid < IPT * nw ? s_base[tid] : 0, s_scan, total);
-        if (tid < IPT * nw) s_base[tid] = mine;
-        __syncthreads();
-        return total;
+        const int mine = cta_exclusive_sum(tid < IPT * nw ? at[tid] : 0, s_scan[which], all);
+        if (tid < IPT * nw) at[tid] = mine;
+        if (tid == 0) s_total[which] = all;
+        cluster_sync();
+        if (nsplit == 1) return 0;
+        const int x = lane < nsplit ? *cg::this_cluster().map_shared_rank(&s_total[which], lane) : 0;
+        all = __reduce_add_sync(0xffffffffu, x);
+        return __reduce_add_sync(0xffffffffu, lane < split ? x : 0);
     };
     // candidates: the middle blocks of a sequence that is trimmed
     uint32_t cand = 0u, keep = 0u;
 #pragma unroll
     for (int i = 0; i < IPT; ++i) {
-        const int j = i * nt + tid;
+        const int j = jt + i * nt;
         if (j < n) {
             if (!trim || j < sink || j >= n - recent)
                 keep |= 1u << i;
@@ -198,105 +216,129 @@ __global__ void __launch_bounds__(1024) cache_evict_kernel(
                 cand |= 1u << i;
         }
     }
-    if (trim) {  // the same for every thread of the CTA
-        const int m = budget - sink - recent;  // candidates to keep, fewer than there are
-        if (m > 0) {
-            uint32_t t = 0u, known = 0u;  // digits found so far, and their bits
-            int need = m;                 // entries still to take among those that match t
-#pragma unroll 1
-            for (int pass = 0; pass < 3; ++pass) {
-                const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-                const uint32_t digits = pass == 2 ? 1023u : 2047u;
-                for (int e = tid; e < kBins; e += nt) s_hist[e] = 0;
-                __syncthreads();
+    const int m = budget - sink - recent;  // candidates to keep, fewer than there are
+    if (trim && m > 0) {                   // the same for every thread of the cluster
+        uint32_t key[IPT];
 #pragma unroll
-                for (int i = 0; i < IPT; ++i) {
-                    const bool on = ((cand >> i) & 1u) && (key[i] & known) == t;
-                    const uint32_t act = __ballot_sync(0xffffffffu, on);
-                    if (act == 0u) continue;
+        for (int i = 0; i < IPT; ++i) key[i] = weight_key(w[i]);
+        uint32_t t = 0u, known = 0u;  // digits found so far, and their bits
+        int need = m;                 // entries still to take among those that match t
+        bool whole = false;           // all that match t are taken
+        for (int e = tid; e < kBins; e += nt) s_own[e] = 0;
+        if (nsplit > 1)
+            for (int e = tid; e < 3 * kBins; e += nt) s_sum[0][e] = 0;
+        cluster_sync();
+#pragma unroll 1
+        for (int pass = 0; pass < 3 && !whole; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+            const uint32_t digits = pass == 2 ? 1023u : 2047u;
+#pragma unroll
+            for (int i = 0; i < IPT; ++i) {
+                const bool on = ((cand >> i) & 1u) && (key[i] & known) == t;
+                const uint32_t act = __ballot_sync(0xffffffffu, on);
+                if (act != 0u) {
                     const uint32_t d = (key[i] >> shift) & digits;
                     const int first = __ffs(act) - 1;
                     const uint32_t d0 = __shfl_sync(0xffffffffu, d, first);
                     const uint32_t same = __ballot_sync(0xffffffffu, on && d == d0);
                     if (lane == first)
-                        atomicAdd(&s_hist[d0], __popc(same));
+                        atomicAdd(&s_own[d0], __popc(same));
                     else if (on && d != d0)
-                        atomicAdd(&s_hist[d], 1);
+                        atomicAdd(&s_own[d], 1);
                 }
-                __syncthreads();
-                // the bin, from the largest down, in which the need-th entry lies
-                const int per = (kBins + nt - 1) / nt;
-                int sum = 0;
-                for (int e = 0; e < per; ++e) {
-                    const int r = tid * per + e;
-                    if (r < kBins) sum += s_hist[kBins - 1 - r];
-                }
-                int all;
-                int before = cta_exclusive_sum(sum, s_scan, all);
-                if (before < need && before + sum >= need) {  // one thread
-                    for (int e = 0; e < per; ++e) {
-                        const int c = s_hist[kBins - 1 - (tid * per + e)];
-                        if (before + c >= need) {
-                            s_pick[0] = kBins - 1 - (tid * per + e);
-                            s_pick[1] = before;
-                            break;
-                        }
-                        before += c;
+            }
+            __syncthreads();
+            // bins from the largest down: thread t has kBins - 1 - t * per and below
+            const int per = (kBins + nt - 1) / nt;
+            const int* hist = s_own;
+            if (nsplit > 1) {
+                for (int e = tid; e < kBins; e += nt) {
+                    const int x = s_own[e];
+                    if (x != 0) {
+                        s_own[e] = 0;  // for the next digit
+                        for (int c = 0; c < nsplit; ++c)
+                            atomicAdd(cg::this_cluster().map_shared_rank(&s_sum[pass][e], c), x);
                     }
                 }
-                __syncthreads();
-                t |= (uint32_t)s_pick[0] << shift;
-                known |= digits << shift;
-                need -= s_pick[1];
+                cg::this_cluster().sync();
+                hist = s_sum[pass];
             }
-            uint32_t ties = 0u;
-#pragma unroll
-            for (int i = 0; i < IPT; ++i)
-                if ((cand >> i) & 1u) {
-                    if (key[i] > t)
-                        keep |= 1u << i;
-                    else if (key[i] == t)
-                        ties |= 1u << i;
+            int sum = 0;
+            for (int e = 0; e < per; ++e) {
+                const int r = tid * per + e;
+                sum += r < kBins ? hist[kBins - 1 - r] : 0;
+            }
+            int all;
+            int before = cta_exclusive_sum(sum, s_scan[pass & 1], all);
+            if (before < need && before + sum >= need) {  // one thread
+                for (int e = 0; e < per; ++e) {
+                    const int bin = kBins - 1 - (tid * per + e);
+                    const int x = hist[bin];
+                    if (before + x >= need) {
+                        s_pick[0] = bin;
+                        s_pick[1] = before;
+                        s_pick[2] = x;
+                        break;
+                    }
+                    before += x;
                 }
-            prefix(ties);
+            }
+            __syncthreads();
+            t |= (uint32_t)s_pick[0] << shift;
+            known |= digits << shift;
+            need -= s_pick[1];
+            whole = s_pick[2] == need;
+            if (nsplit == 1 && pass < 2 && !whole) {
+                for (int e = tid; e < kBins; e += nt) s_own[e] = 0;
+                __syncthreads();
+            }
+        }
+        uint32_t ties = 0u;
+#pragma unroll
+        for (int i = 0; i < IPT; ++i)
+            if ((cand >> i) & 1u) {
+                if ((key[i] & known) > t || (whole && (key[i] & known) == t))
+                    keep |= 1u << i;
+                else if (key[i] == t)
+                    ties |= 1u << i;
+            }
+        if (!whole) {  // the lowest `need` of the tied blocks
+            int all;
+            const int lower = prefix(ties, 0, all);
 #pragma unroll
             for (int i = 0; i < IPT; ++i) {
                 const uint32_t v = __ballot_sync(0xffffffffu, (ties >> i) & 1u);
-                if (((ties >> i) & 1u) && s_base[i * nw + warp] + __popc(v & below) < need)
-                    keep |= 1u << i;  // the lowest blocks first
+                if (((ties >> i) & 1u) && lower + s_base[0][i * nw + warp] + __popc(v & below) < need)
+                    keep |= 1u << i;
             }
-            __syncthreads();  // s_base is written again
         }
     }
-    int page[IPT];
-    float w[IPT];
-#pragma unroll
-    for (int i = 0; i < IPT; ++i) {  // read again (from L2): not held through the search
-        const int j = i * nt + tid;
-        page[i] = j < nb_max ? table[base + j] : 0;
-        w[i] = j < nb_max ? weight[base + j] : 0.f;
-    }
-    const int n_keep = prefix(keep);  // its barriers stand between the reads and the writes
+    int n_keep;
+    const int lower = prefix(keep, 1, n_keep);  // its barrier stands between the reads and the writes
+    int32_t* tout = table_out + (size_t)b * nb_max;
+    float* wout = weight_out + (size_t)b * nb_max;
+    int32_t* kept = kept_ids ? kept_ids + (size_t)b * budget : nullptr;
 #pragma unroll
     for (int i = 0; i < IPT; ++i) {
-        const int j = i * nt + tid;
+        const int j = jt + i * nt;
         const bool k = (keep >> i) & 1u;
         const uint32_t v = __ballot_sync(0xffffffffu, k);
-        const int pos = s_base[i * nw + warp] + __popc(v & below);  // kept blocks before j
+        const int pos = lower + s_base[1][i * nw + warp] + __popc(v & below);  // kept blocks before j
         if (j < nb_max) {
             const int to = j >= n ? j : k ? pos : n_keep + (j - pos);
-            table_out[base + to] = page[i];
-            weight_out[base + to] = k || bad ? w[i] : 0.f;
-            if (k && kept_ids && pos < budget) kept_ids[(size_t)b * budget + pos] = j;
+            tout[to] = page[i];
+            wout[to] = k || bad ? w[i] : 0.f;
+            if (k && kept && pos < budget) kept[pos] = j;
         }
     }
-    if (kept_ids)
-        for (int i = n_keep + tid; i < budget; i += nt) kept_ids[(size_t)b * budget + i] = -1;
-    if (tid == 0) {
+    if (kept)
+        for (int i = n_keep + split * nt + tid; i < budget; i += nsplit * nt) kept[i] = -1;
+    if (split == 0 && tid == 0) {
         const int gone = n - n_keep;
         ctx_out[b] = ctx - gone * bs;
         if (freed) freed[b] = gone;
     }
+    if (nsplit > 1) cg::this_cluster().sync();  // no CTA leaves while its counts are read
 }
 
 }  // namespace lci

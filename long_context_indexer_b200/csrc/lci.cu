@@ -1514,10 +1514,13 @@ cudaError_t launch_evict(const lci_block_table* t, int32_t batch, const int32_t*
                          const float* weight, int32_t budget, int32_t sink, int32_t recent,
                          int32_t* table_out, int32_t* ctx_out, float* weight_out, int32_t* kept,
                          int32_t* freed, cudaStream_t st) {
-    const int threads = ((t->max_blocks + IPT - 1) / IPT + 31) / 32 * 32;
-    return launch_early(lci::cache_evict_kernel<IPT>, dim3((unsigned)batch), dim3(threads), 0, st, 1,
-                        t->d_table, ctx_len, weight, t->max_blocks, t->block_size, budget, sink,
-                        recent, table_out, ctx_out, weight_out, kept, freed);
+    // one CTA up to 1024 blocks, then a cluster of up to 8
+    const int rows = (t->max_blocks + IPT - 1) / IPT;
+    const int nsplit = (rows + 1023) / 1024;
+    const int threads = ((rows + nsplit - 1) / nsplit + 31) / 32 * 32;
+    return launch_early(lci::cache_evict_kernel<IPT>, dim3((unsigned)batch * nsplit), dim3(threads), 0,
+                        st, nsplit, t->d_table, ctx_len, weight, t->max_blocks, t->block_size, budget,
+                        sink, recent, table_out, ctx_out, weight_out, kept, freed, nsplit);
 }
 
 }  // namespace
@@ -1687,9 +1690,8 @@ lci_status lci_cache_evict(const lci_block_table* table, int32_t batch, const in
         return fail(LCI_ERR_UNSUPPORTED, "cache_evict: max_blocks %d above %d", table->max_blocks,
                     kMaxNbMax);
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    // blocks per thread: up to 1024 threads
-    const int nb = table->max_blocks;
-    auto run = nb <= 1024 ? launch_evict<1> : nb <= 4096 ? launch_evict<4> : launch_evict<16>;
+    // one block per thread in up to 8 CTAs of 1024, then two
+    auto run = table->max_blocks <= 8192 ? launch_evict<1> : launch_evict<2>;
     const cudaError_t e = run(table, batch, d_ctx_len, d_weight, budget, sink, recent, d_table_out,
                               d_ctx_out, d_weight_out, d_kept, d_freed, cs);
     if (e != cudaSuccess) return fail(LCI_ERR_CUDA, "cache_evict: %s", cudaGetErrorString(e));
