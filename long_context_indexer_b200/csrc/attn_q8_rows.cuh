@@ -89,6 +89,30 @@ __device__ __forceinline__ VScale split_v_scale(float vs) {
     return r;
 }
 
+// Merges n <= N partial softmax results of head h, given as [partial][16][max,
+// sum]: the maximum, the sum and each partial's factor.
+template <int N>
+struct Q8Merge {
+    float f[N], M, L;
+    __device__ __forceinline__ Q8Merge(const float* ml, int n, int h) {
+        float2 v[N];
+        M = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            v[i] = i < n ? *reinterpret_cast<const float2*>(ml + (i * q8r::kRows + h) * 2)
+                         : make_float2(-INFINITY, 0.f);
+            M = fmaxf(M, v[i].x);
+        }
+        const float base = M == -INFINITY ? 0.f : M;
+        L = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            f[i] = fast_exp2(v[i].x - base);
+            L = fmaf(f[i], v[i].y, L);
+        }
+    }
+};
+
 // One strip's raw codes, as this lane's MMA fragments need them.
 template <int HD>
 struct Q8Strip {
@@ -156,24 +180,98 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
         __syncthreads();
     }
 
+    // The loads that depend on nothing go first, all in flight together: the
+    // ids of this warp's first 32 blocks, the query rows, the positions.
+    const int32_t* row_ids = a.ids + (size_t)row * a.topk + i0;
+    const int blk_end = w1 > w0 ? (w1 - 1) / spb + 1 : 0;
+    int base = w1 > w0 ? w0 / spb : 0;  // blocks are looked up 32 at a time, one per lane
+    const int j_first = base + lane < blk_end ? row_ids[base + lane] : -1;
+    uint4 qraw[2][HD / 64][2];
+    {
+        const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(a.q) + ((size_t)row * a.H_q + (size_t)g * G) * HD;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int c = 0; c < HD / 64; ++c)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    qraw[r][c][x] = g8 + 8 * r < G ? __ldg(reinterpret_cast<const uint4*>(
+                                                         qrow + (size_t)(g8 + 8 * r) * HD + 16 * (q4 + 4 * c) + 8 * x))
+                                                   : make_uint4(0, 0, 0, 0);
+    }
+    const Q8Window win = q8_window(a, row, b, s);
+    float slope_a = 0.f, slope_b = 0.f, inv_cap = 0.f;
+    if constexpr (MODS) {
+        inv_cap = a.cap > 0.f ? 1.f / a.cap : 0.f;
+        if (a.slopes) {
+            slope_a = g8 < G ? a.slopes[g * G + g8] : 0.f;
+            slope_b = g8 + 8 < G ? a.slopes[g * G + g8 + 8] : 0.f;
+        }
+    }
+
+
+    // The load cursor, one strip ahead of the compute: block (of this CTA),
+    // strips left of it, its first token, scales and pointers.
+    int t_lane = -1;
+    unsigned long long cell_lane = 0;
+    float ks_lane = 0.f, vs_lane = 0.f;
+    uint32_t live = 0u;
+    int n_blk = -1, st = 0, st_end = 0, n_t0 = 0;
+    float n_ks = 0.f, n_vs = 0.f;
+    const uint8_t *kp = nullptr, *vp = nullptr;
+    auto lookup = [&](int j) {
+        t_lane = -1;
+        const int page = q8_page(a, b, j, win);
+        if (page >= 0) {
+            t_lane = j * a.bs;
+            cell_lane = (unsigned long long)page * a.H_kv + g;
+            ks_lane = a.ks[cell_lane];
+            vs_lane = a.vs[cell_lane];
+        }
+        live = __ballot_sync(0xffffffffu, t_lane >= 0);
+    };
+    auto advance = [&]() -> bool {  // to the next strip in the window; false: none left
+        if (++st < st_end) return true;
+        for (;;) {
+            while (live) {
+                const int x = __ffs(live) - 1;
+                live &= live - 1u;
+                n_blk = base + x;
+                n_t0 = __shfl_sync(0xffffffffu, t_lane, x);
+                n_ks = __shfl_sync(0xffffffffu, ks_lane, x);
+                n_vs = __shfl_sync(0xffffffffu, vs_lane, x);
+                const unsigned long long c = __shfl_sync(0xffffffffu, cell_lane, x);
+                kp = a.k + c * a.bs * HD;
+                vp = a.v + c * a.bs * HD;
+                // this warp's strips, cut to the window
+                const int lo = win.lo - n_t0, hi = win.hi - n_t0;
+                st = max(w0 - n_blk * spb, lo > 0 ? lo / kStrip : 0);
+                st_end = min(min(w1 - n_blk * spb, spb), hi / kStrip + 1);
+                if (st < st_end) return true;
+            }
+            base += 32;
+            if (base >= blk_end) return false;
+            lookup(base + lane < blk_end ? row_ids[base + lane] : -1);
+        }
+    };
+    Q8Strip<HD> cur, nxt;
+    lookup(j_first);
+    bool have = blk_end > 0 && advance();
+    if (have) cur.load(kp + (size_t)st * kStrip * HD, vp + (size_t)st * kStrip * HD, g8, q4);
+
     // the group's query rows, scaled to f16 (head rows g8 and g8 + 8)
     uint32_t qf[KS][4];
     float qs_a, qs_b;  // what a row's logits are multiplied by (with the softmax scale)
     {
-        const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(a.q) + ((size_t)row * a.H_q + (size_t)g * G) * HD;
         float back[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const int h = g8 + 8 * r;
-            uint4 w[HD / 64][2];
             float amax = 0.f;
 #pragma unroll
             for (int c = 0; c < HD / 64; ++c)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    w[c][x] = h < G ? __ldg(reinterpret_cast<const uint4*>(qrow + (size_t)h * HD + 16 * (q4 + 4 * c) + 8 * x))
-                                    : make_uint4(0, 0, 0, 0);
-                    const uint32_t u[4] = {w[c][x].x, w[c][x].y, w[c][x].z, w[c][x].w};
+                    const uint32_t u[4] = {qraw[r][c][x].x, qraw[r][c][x].y, qraw[r][c][x].z, qraw[r][c][x].w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float2 f = bf16x2_to_f32(u[k]);
@@ -191,7 +289,7 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
             for (int c = 0; c < HD / 64; ++c)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const uint32_t u[4] = {w[c][x].x, w[c][x].y, w[c][x].z, w[c][x].w};
+                    const uint32_t u[4] = {qraw[r][c][x].x, qraw[r][c][x].y, qraw[r][c][x].z, qraw[r][c][x].w};
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {  // k-step 4c + 2x + k: dims 4k .. 4k+3 of the run's half
                         const float2 lo = bf16x2_to_f32(u[2 * k]), hi = bf16x2_to_f32(u[2 * k + 1]);
@@ -204,16 +302,6 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
         qs_a = unit * back[0];
         qs_b = unit * back[1];
     }
-    const Q8Window win = q8_window(a, row, b, s);
-    float slope_a = 0.f, slope_b = 0.f, inv_cap = 0.f;
-    if constexpr (MODS) {
-        inv_cap = a.cap > 0.f ? 1.f / a.cap : 0.f;
-        if (a.slopes) {
-            slope_a = g8 < G ? a.slopes[g * G + g8] : 0.f;
-            slope_b = g8 + 8 < G ? a.slopes[g * G + g8 + 8] : 0.f;
-        }
-    }
-
     float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;  // l: this lane's share
     float r_a = 0.f, r_b = 0.f;                                    // the current block's share
     float o[ON][4];
@@ -238,169 +326,124 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
         r_a = r_b = 0.f;
     };
 
-    const int32_t* row_ids = a.ids + (size_t)row * a.topk + i0;
-    const int blk_end = w1 > w0 ? (w1 - 1) / spb + 1 : 0;
-    // blocks of this warp in batches of 32: lanes look up pages and scales
-    for (int base = w1 > w0 ? w0 / spb : 0; base < blk_end; base += 32) {
-        int t_lane = -1;
-        size_t cell = 0;
-        float ks = 0.f, vs = 0.f;
-        if (base + lane < blk_end) {
-            const int j = row_ids[base + lane];
-            const int page = q8_page(a, b, j, win);
-            if (page >= 0) {
-                t_lane = j * a.bs;
-                cell = (size_t)page * a.H_kv + g;
-                ks = a.ks[cell];
-                vs = a.vs[cell];
-            }
-        }
-        uint32_t live = __ballot_sync(0xffffffffu, t_lane >= 0);
-        if (live == 0u) continue;
-        // block, strip and pointers of the load cursor, one strip ahead of the compute
-        int blk = -1, st = 0, st_end = 0;
-        const uint8_t *kp = nullptr, *vp = nullptr;
-        int t_first = 0;
-        auto enter = [&](int x) {  // strip range and pointers of batch entry x
-            blk = x;
-            const int first = (base + x) * spb;
-            t_first = __shfl_sync(0xffffffffu, t_lane, x);
-            const unsigned long long c = __shfl_sync(0xffffffffu, (unsigned long long)cell, x);
-            kp = a.k + c * a.bs * HD;
-            vp = a.v + c * a.bs * HD;
-            // strips of this warp, cut to the window
-            st = max(w0 - first, 0);
-            st_end = min(w1 - first, spb);
-            const int lo = win.lo - t_first, hi = win.hi - t_first;
-            if (lo > 0) st = max(st, lo / kStrip);
-            st_end = min(st_end, hi / kStrip + 1);
-        };
-        auto next_block = [&]() -> bool {  // to the first strip of the next live block
-            while (live) {
-                const int x = __ffs(live) - 1;
-                live &= live - 1u;
-                enter(x);
-                if (st < st_end) return true;
-            }
-            return false;
-        };
-        Q8Strip<HD> cur, nxt;
-        bool have = next_block();
-        if (have) cur.load(kp + (size_t)st * kStrip * HD, vp + (size_t)st * kStrip * HD, g8, q4);
-        while (have) {
-            const int c_blk = blk, c_t0 = t_first + st * kStrip;
-            bool more = true;
-            ++st;
-            if (st >= st_end) more = next_block();
-            if (more) nxt.load(kp + (size_t)st * kStrip * HD, vp + (size_t)st * kStrip * HD, g8, q4);
-            const float c_ks = __shfl_sync(0xffffffffu, ks, c_blk);
-            const VScale c_vs = split_v_scale(__shfl_sync(0xffffffffu, vs, c_blk));
+    while (have) {
+        const int c_blk = n_blk, c_t0 = n_t0 + st * kStrip;
+        const float c_ks = n_ks;
+        const VScale c_vs = split_v_scale(n_vs);
+        const bool more = advance();
+        if (more) nxt.load(kp + (size_t)st * kStrip * HD, vp + (size_t)st * kStrip * HD, g8, q4);
 
-            // S = Q K^T: two n-tiles of 8 tokens
-            float sc[2][4];
+        // S = Q K^T: two n-tiles of 8 tokens
+        // in two chains each (even and odd k-steps)
+        float sc[2][4], sd[2][4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[j][e] = 0.f;
+            for (int e = 0; e < 4; ++e) sc[j][e] = sd[j][e] = 0.f;
 #pragma unroll
-                for (int c = 0; c < HD / 64; ++c) {
+        for (int c = 0; c < HD / 64; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
                     const uint32_t w[4] = {cur.k[j][c].x, cur.k[j][c].y, cur.k[j][c].z, cur.k[j][c].w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f16_16816(sc[j], qf[4 * c + k], e4m3x2_to_f16x2(w[k]), e4m3x2_to_f16x2(w[k] >> 16));
+                    mma_f16_16816(k & 1 ? sd[j] : sc[j], qf[4 * c + k], e4m3x2_to_f16x2(w[k]),
+                                  e4m3x2_to_f16x2(w[k] >> 16));
                 }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[j][e] += sd[j][e];
+        // logits in log2 units, plus the v scale's exponent
+        const float ca = qs_a * c_ks, cb = qs_b * c_ks;
+        float x[2][4];
+        const int ta = c_t0 + 2 * q4;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float z = sc[j][e] * (e < 2 ? ca : cb);
+                if constexpr (MODS)
+                    x[j][e] = q8_score(z, a.cap, inv_cap, e < 2 ? slope_a : slope_b,
+                                       abs(win.p - (ta + 8 * j + (e & 1)))) + c_vs.e;
+                else
+                    x[j][e] = z + c_vs.e;
             }
-            // logits in log2 units, plus the v scale's exponent
-            const float ca = qs_a * c_ks, cb = qs_b * c_ks;
-            float x[2][4];
-            const int ta = c_t0 + 2 * q4;
+        const bool partial = c_t0 < win.lo || c_t0 + kStrip - 1 > win.hi;
+        if (partial) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float z = sc[j][e] * (e < 2 ? ca : cb);
-                    if constexpr (MODS)
-                        x[j][e] = q8_score(z, a.cap, inv_cap, e < 2 ? slope_a : slope_b,
-                                           abs(win.p - (ta + 8 * j + (e & 1)))) + c_vs.e;
-                    else
-                        x[j][e] = z + c_vs.e;
-                }
-            const bool partial = c_t0 < win.lo || c_t0 + kStrip - 1 > win.hi;
-            if (partial) {
+                for (int e = 0; e < 2; ++e) {
+                    const int t = ta + 8 * j + e;
+                    if (t < win.lo || t > win.hi) {
+                        x[j][e] = x[j][e + 2] = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int t = ta + 8 * j + e;
-                        if (t < win.lo || t > win.hi) {
-                            x[j][e] = x[j][e + 2] = -INFINITY;
-#pragma unroll
-                            for (int w = 0; w < HD / 32; ++w) cur.v[2 * j + e][w] = 0u;  // unset memory
-                        }
+                        for (int w = 0; w < HD / 32; ++w) cur.v[2 * j + e][w] = 0u;  // unset memory
                     }
-            }
-            float mx_a = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-            float mx_b = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
-            mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 1));
-            mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, 1));
-            mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 2));
-            mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, 2));
-            const bool up_a = mx_a > m_a + kLazy, up_b = mx_b > m_b + kLazy;
-            if (__any_sync(0xffffffffu, up_a || up_b)) {
-                const float co_a = up_a ? exp2f(m_a - mx_a) : 1.f, co_b = up_b ? exp2f(m_b - mx_b) : 1.f;
-                m_a = up_a ? mx_a : m_a;
-                m_b = up_b ? mx_b : m_b;
-                l_a *= co_a;
-                l_b *= co_b;
-                r_a *= co_a;
-                r_b *= co_b;
-#pragma unroll
-                for (int i = 0; i < ON; ++i) {
-                    o[i][0] *= co_a;
-                    o[i][1] *= co_a;
-                    o[i][2] *= co_b;
-                    o[i][3] *= co_b;
                 }
-            }
-            const float base_a = m_a == -INFINITY ? 0.f : m_a, base_b = m_b == -INFINITY ? 0.f : m_b;
-            float p[2][4], sum_a = 0.f, sum_b = 0.f;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                p[j][0] = fast_exp2(x[j][0] - base_a);
-                p[j][1] = fast_exp2(x[j][1] - base_a);
-                p[j][2] = fast_exp2(x[j][2] - base_b);
-                p[j][3] = fast_exp2(x[j][3] - base_b);
-                sum_a += p[j][0] + p[j][1];
-                sum_b += p[j][2] + p[j][3];
-            }
-            sum_a *= c_vs.inv;
-            sum_b *= c_vs.inv;
-            l_a += sum_a;
-            l_b += sum_b;
-            r_a += sum_a;
-            r_b += sum_b;
-            uint32_t pf[4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                pf[2 * j] = pack_f16x2(p[j][0] * c_vs.f, p[j][1] * c_vs.f);
-                pf[2 * j + 1] = pack_f16x2(p[j][2] * c_vs.f, p[j][3] * c_vs.f);
-            }
-            // O += P V
-#pragma unroll
-            for (int w = 0; w < HD / 32; ++w) {
-                const uint32_t ab0 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x5140);
-                const uint32_t ab1 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x7362);
-                const uint32_t cd0 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x5140);
-                const uint32_t cd1 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x7362);
-                mma_f16_16816(o[4 * w], pf, e4m3x2_to_f16x2(ab0), e4m3x2_to_f16x2(cd0));
-                mma_f16_16816(o[4 * w + 1], pf, e4m3x2_to_f16x2(ab0 >> 16), e4m3x2_to_f16x2(cd0 >> 16));
-                mma_f16_16816(o[4 * w + 2], pf, e4m3x2_to_f16x2(ab1), e4m3x2_to_f16x2(cd1));
-                mma_f16_16816(o[4 * w + 3], pf, e4m3x2_to_f16x2(ab1 >> 16), e4m3x2_to_f16x2(cd1 >> 16));
-            }
-            if (!more || blk != c_blk) close_block(base + c_blk);
-            have = more;
-            cur = nxt;
         }
+        float mx_a = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
+        float mx_b = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
+        mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 1));
+        mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, 1));
+        mx_a = fmaxf(mx_a, __shfl_xor_sync(0xffffffffu, mx_a, 2));
+        mx_b = fmaxf(mx_b, __shfl_xor_sync(0xffffffffu, mx_b, 2));
+        const bool up_a = mx_a > m_a + kLazy, up_b = mx_b > m_b + kLazy;
+        if (__any_sync(0xffffffffu, up_a || up_b)) {
+            const float co_a = up_a ? exp2f(m_a - mx_a) : 1.f, co_b = up_b ? exp2f(m_b - mx_b) : 1.f;
+            m_a = up_a ? mx_a : m_a;
+            m_b = up_b ? mx_b : m_b;
+            l_a *= co_a;
+            l_b *= co_b;
+            r_a *= co_a;
+            r_b *= co_b;
+#pragma unroll
+            for (int i = 0; i < ON; ++i) {
+                o[i][0] *= co_a;
+                o[i][1] *= co_a;
+                o[i][2] *= co_b;
+                o[i][3] *= co_b;
+            }
+        }
+        const float base_a = m_a == -INFINITY ? 0.f : m_a, base_b = m_b == -INFINITY ? 0.f : m_b;
+        float p[2][4], sum_a = 0.f, sum_b = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            p[j][0] = fast_exp2(x[j][0] - base_a);
+            p[j][1] = fast_exp2(x[j][1] - base_a);
+            p[j][2] = fast_exp2(x[j][2] - base_b);
+            p[j][3] = fast_exp2(x[j][3] - base_b);
+            sum_a += p[j][0] + p[j][1];
+            sum_b += p[j][2] + p[j][3];
+        }
+        sum_a *= c_vs.inv;
+        sum_b *= c_vs.inv;
+        l_a += sum_a;
+        l_b += sum_b;
+        r_a += sum_a;
+        r_b += sum_b;
+        uint32_t pf[4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            pf[2 * j] = pack_f16x2(p[j][0] * c_vs.f, p[j][1] * c_vs.f);
+            pf[2 * j + 1] = pack_f16x2(p[j][2] * c_vs.f, p[j][3] * c_vs.f);
+        }
+        // O += P V
+#pragma unroll
+        for (int w = 0; w < HD / 32; ++w) {
+            const uint32_t ab0 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x5140);
+            const uint32_t ab1 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x7362);
+            const uint32_t cd0 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x5140);
+            const uint32_t cd1 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x7362);
+            mma_f16_16816(o[4 * w], pf, e4m3x2_to_f16x2(ab0), e4m3x2_to_f16x2(cd0));
+            mma_f16_16816(o[4 * w + 1], pf, e4m3x2_to_f16x2(ab0 >> 16), e4m3x2_to_f16x2(cd0 >> 16));
+            mma_f16_16816(o[4 * w + 2], pf, e4m3x2_to_f16x2(ab1), e4m3x2_to_f16x2(cd1));
+            mma_f16_16816(o[4 * w + 3], pf, e4m3x2_to_f16x2(ab1 >> 16), e4m3x2_to_f16x2(cd1 >> 16));
+        }
+        if (!more || n_blk != c_blk) close_block(c_blk);
+        have = more;
+        cur = nxt;
     }
 
     // ---- the warps' partials: (max, sum) and O in shared memory ----
@@ -431,16 +474,9 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
     const int groups = G * (HD / 4);  // float4 groups of the pair's output
     const int share = (groups + nsplit - 1) / nsplit;
     __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) + ((size_t)row * a.H_q + (size_t)g * G) * HD;
-    auto merged = [&](const float* ml, int n, int h, float& M) -> float {  // max and sum over n partials
-        M = -INFINITY;
-        for (int w = 0; w < n; ++w) M = fmaxf(M, ml[(w * kRows + h) * 2]);
-        const float base = M == -INFINITY ? 0.f : M;
-        float L = 0.f;
-        for (int w = 0; w < n; ++w) L += exp2f(ml[(w * kRows + h) * 2] - base) * ml[(w * kRows + h) * 2 + 1];
-        return L;
-    };
+    // L == 0: nothing attended, a zero row; a NaN sum stays NaN
     auto write4 = [&](int q, float4 v, float L) {
-        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const float inv = 1.f / L;
         uint2 w = make_uint2(0u, 0u);
         if (L != 0.f) {
             w.x = pack_bf16x2(v.x * inv, v.y * inv);
@@ -448,87 +484,89 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
         }
         *reinterpret_cast<uint2*>(orow + 4 * q) = w;
     };
+    if (nsplit > 1 && warp == NW - 1) {
+        // this CTA's (max, sum) of every head to every CTA of the cluster
+        for (int e = lane; e < G * nsplit; e += 32) {
+            const int h = e % G, to = e / G;
+            const Q8Merge<NW> mg(sml, NW, h);
+            float* dst = cg::this_cluster().map_shared_rank(cml, to) + (split * kRows + h) * 2;
+            *reinterpret_cast<float2*>(dst) = make_float2(mg.M, mg.L);
+        }
+    }
     for (int q = tid; q < groups; q += NT) {
         const int h = q / (HD / 4), c = q - h * (HD / 4);
         const int seg = c / (HD / 16), in = c - seg * (HD / 16);
         const float* src = so + h * row_pitch<HD>() + seg * seg_pitch<HD>() + 4 * in;
-        float M;
-        const float L = merged(sml, NW, h, M);
-        const float base = M == -INFINITY ? 0.f : M;
+        const Q8Merge<NW> mg(sml, NW, h);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            const float f = exp2f(sml[(w * kRows + h) * 2] - base);
             const float4 v = *reinterpret_cast<const float4*>(src + w * kRows * row_pitch<HD>());
-            acc.x += f * v.x;
-            acc.y += f * v.y;
-            acc.z += f * v.z;
-            acc.w += f * v.w;
+            acc.x += mg.f[w] * v.x;
+            acc.y += mg.f[w] * v.y;
+            acc.z += mg.f[w] * v.z;
+            acc.w += mg.f[w] * v.w;
         }
         if (nsplit == 1) {
-            write4(q, acc, L);
+            write4(q, acc, mg.L);
         } else {
             const int owner = q / share;
             float* dst = cg::this_cluster().map_shared_rank(recv, owner) + (size_t)(split * share + q - owner * share) * 4;
             *reinterpret_cast<float4*>(dst) = acc;
         }
     }
-    const float* ml = sml;  // partials the pair's max and sum come from
-    int nml = NW;
     if (nsplit > 1) {
-        if (tid < G * nsplit) {  // this CTA's (max, sum) to every CTA
-            const int h = tid % G, to = tid / G;
-            float M;
-            const float L = merged(sml, NW, h, M);
-            float* dst = cg::this_cluster().map_shared_rank(cml, to) + (split * kRows + h) * 2;
-            *reinterpret_cast<float2*>(dst) = make_float2(M, L);
-        }
         cluster_arrive();
         cluster_wait();
-        ml = cml;
-        nml = nsplit;
+    }
+    // per head, for the lse and the masses: the pair's maximum and 1 / sum
+    float2* fin = reinterpret_cast<float2*>(so);  // O partials have been read
+    if (nsplit == 1 && mass) __syncthreads();
+    if (warp == NW - 1 && lane < G) {
+        const Q8Merge<NW> one(sml, NW, lane);
+        const Q8Merge<kMaxSplit> all(cml, nsplit, lane);
+        const float M = nsplit == 1 ? one.M : all.M, L = nsplit == 1 ? one.L : all.L;
+        if (a.lse && split == 0)
+            a.lse[(size_t)row * a.H_q + (size_t)g * G + lane] = L == 0.f ? -INFINITY : M + log2f(L);
+        if (mass) fin[lane] = make_float2(M == -INFINITY ? 0.f : M, L == 0.f ? 0.f : 1.f / L);
+    }
+    if (nsplit > 1) {
         for (int q = split * share + tid; q < min(groups, (split + 1) * share); q += NT) {
-            const int h = q / (HD / 4);
-            float M;
-            const float L = merged(cml, nsplit, h, M);
-            const float base = M == -INFINITY ? 0.f : M;
+            const Q8Merge<kMaxSplit> mg(cml, nsplit, q / (HD / 4));
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int r = 0; r < nsplit; ++r) {
-                const float f = exp2f(cml[(r * kRows + h) * 2] - base);
-                const float4 v = *reinterpret_cast<const float4*>(recv + (size_t)(r * share + q - split * share) * 4);
-                acc.x += f * v.x;
-                acc.y += f * v.y;
-                acc.z += f * v.z;
-                acc.w += f * v.w;
-            }
-            write4(q, acc, L);
+#pragma unroll
+            for (int r = 0; r < kMaxSplit; ++r)
+                if (r < nsplit) {
+                    const float4 v = *reinterpret_cast<const float4*>(recv + (size_t)(r * share + q - split * share) * 4);
+                    acc.x += mg.f[r] * v.x;
+                    acc.y += mg.f[r] * v.y;
+                    acc.z += mg.f[r] * v.z;
+                    acc.w += mg.f[r] * v.w;
+                }
+            write4(q, acc, mg.L);
         }
     }
-    if (a.lse && split == 0 && tid < G) {
-        float M;
-        const float L = merged(ml, nml, tid, M);
-        a.lse[(size_t)row * a.H_q + (size_t)g * G + tid] = L == 0.f ? -INFINITY : M + log2f(L);
-    }
     if (mass) {
-        // mass of block i: over the warps that met it and the group's heads
+        __syncthreads();
+        // mass of block i: over the warps that met it and the group's heads,
+        // four lanes sharing a block's heads
         float* mrow = a.mass + ((size_t)row * a.H_kv + g) * a.topk + i0;
-        for (int e = tid; e < nblk * 4; e += NT) {  // four lanes share a block's heads
+        for (int e = tid; e < nblk * 4; e += NT) {
             const int i = e >> 2, part = e & 3;
             const uint32_t quad = 0xfu << (lane & 28);
             float x = 0.f;
             if (wper > 0) {
                 const int wa = (i * spb) / wper, wb = min(NW - 1, (i * spb + spb - 1) / wper);
-                for (int h = part; h < G; h += 4) {
-                    float M;
-                    const float L = merged(ml, nml, h, M);
-                    if (L == 0.f) continue;
-                    const float base = M == -INFINITY ? 0.f : M;
-                    float y = 0.f;
-                    for (int w = wa; w <= wb; ++w) {
-                        const float2 v = *(reinterpret_cast<const float2*>(sbm) + (size_t)(i + w) * kRows + h);
-                        y += exp2f(v.x - base) * v.y;
+                for (int w = wa; w <= wb; ++w) {
+                    const float2* met = reinterpret_cast<const float2*>(sbm) + (size_t)(i + w) * kRows;
+#pragma unroll
+                    for (int k = 0; k < kRows / 4; ++k) {
+                        const int h = part + 4 * k;
+                        if (h < G) {
+                            const float2 v = met[h], f = fin[h];
+                            x += fast_exp2(v.x - f.x) * v.y * f.y;
+                        }
                     }
-                    x += y / L;
                 }
             }
             x += __shfl_xor_sync(quad, x, 1);

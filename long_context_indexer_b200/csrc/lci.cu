@@ -1472,41 +1472,101 @@ bool rows_q8_fits(const lci::AttnQ8Args& a, lci_dtype dtype) {
            a.H_q / a.H_kv <= lci::q8r::kRows;
 }
 
-template <int HD, int NW, bool MODS>
-lci_status launch_attn_q8_rows(const lci::AttnQ8Args& a, long long pairs, int nsplit,
-                               cudaStream_t st) {
-    auto kern = lci::sparse_attn_q8_rows_kernel<HD, NW, MODS>;
-    const int blocks = a.mass ? (a.topk + nsplit - 1) / nsplit : 0;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        (int)lci::q8r::smem_bytes<HD, NW>(lci::kMaxTopk));
-    });
-    if (attr_err != cudaSuccess)
-        return fail(LCI_ERR_CUDA, "sparse_attn_q8: %s", cudaGetErrorString(attr_err));
-    const cudaError_t e = launch_early(kern, dim3((unsigned)(pairs * nsplit)), dim3(NW * 32),
-                                       lci::q8r::smem_bytes<HD, NW>(blocks), st, nsplit, a, nsplit);
-    if (e != cudaSuccess) return fail(LCI_ERR_CUDA, "sparse_attn_q8: %s", cudaGetErrorString(e));
-    return check_launch("sparse_attn_q8");
-}
+// What a kernel needs set up once on every device that runs it: its largest
+// dynamic shared memory, and how many clusters of n CTAs the device holds at
+// once (0 until asked).
+struct KernelSetup {
+    static constexpr int kDevices = 64, kSizes = 17;
+    std::mutex mu;
+    bool ready[kDevices] = {};
+    int clusters[kDevices][kSizes] = {};
 
-// Splits of a pair over a cluster, and warps per CTA.
-struct RowsShape {
-    int nsplit, warps;
+    template <typename K>
+    cudaError_t prepare(K kern, int max_smem, bool wide_clusters = false) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess || dev >= kDevices) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+        std::lock_guard<std::mutex> lock(mu);
+        if (ready[dev]) return cudaSuccess;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
+        if (e == cudaSuccess && wide_clusters)
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        ready[dev] = e == cudaSuccess;
+        return e;
+    }
+    template <typename K>
+    int max_clusters(K kern, int size, int threads, size_t smem) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
+        std::lock_guard<std::mutex> lock(mu);
+        if (clusters[dev][size] == 0) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)size);
+            cfg.blockDim = dim3((unsigned)threads);
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = (unsigned)size;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                n = 0;
+            }
+            clusters[dev][size] = n + 1;
+        }
+        return clusters[dev][size] - 1;
+    }
 };
-RowsShape rows_q8_shape(const lci::AttnQ8Args& a, long long pairs) {
-    long long n = (2 * 148 + pairs - 1) / pairs;
-    n = std::min<long long>({n, (long long)lci::q8r::kMaxSplit, (long long)a.topk});
-    const int nsplit = (int)std::max<long long>(n, 1);
-    return {nsplit, pairs * nsplit <= 148 ? 8 : 4};
-}
 
+// The row-wise kernel with NW warps per CTA: the largest split of a pair (up to
+// 8 CTAs, at most one per block) whose clusters the device holds all at once; a
+// second wave costs more than longer runs per warp (16 pairs: 25.2 us with
+// clusters of 8, of which 16 do not fit, against 17.8 with clusters of 4).
+template <int HD, int NW, bool MODS>
+struct Q8Rows {
+    static KernelSetup setup;
+    static constexpr auto kern = lci::sparse_attn_q8_rows_kernel<HD, NW, MODS>;
+    static size_t smem(const lci::AttnQ8Args& a, int nsplit) {
+        return lci::q8r::smem_bytes<HD, NW>(a.mass ? (a.topk + nsplit - 1) / nsplit : 0);
+    }
+    static cudaError_t prepare() {
+        return setup.prepare(kern, (int)lci::q8r::smem_bytes<HD, NW>(lci::kMaxTopk));
+    }
+    static int best_split(const lci::AttnQ8Args& a, long long pairs) {
+        int n = std::min(lci::q8r::kMaxSplit, a.topk);
+        const size_t most = lci::q8r::smem_bytes<HD, NW>(lci::kMaxTopk);
+        while (n > 1 && setup.max_clusters(kern, n, NW * 32, most) < pairs) --n;
+        return n;
+    }
+    static lci_status launch(const lci::AttnQ8Args& a, long long pairs, int nsplit, cudaStream_t st) {
+        const cudaError_t e = launch_early(kern, dim3((unsigned)(pairs * nsplit)), dim3(NW * 32),
+                                           smem(a, nsplit), st, nsplit, a, nsplit);
+        if (e != cudaSuccess)
+            return fail(LCI_ERR_CUDA, "sparse_attn_q8: %s", cudaGetErrorString(e));
+        return check_launch("sparse_attn_q8");
+    }
+};
+template <int HD, int NW, bool MODS> KernelSetup Q8Rows<HD, NW, MODS>::setup;
+
+// Few pairs: eight warps per CTA, one CTA per SM, as many CTAs per pair as fit.
+// Else four warps per CTA, two CTAs per SM, each pair whole once they fill the
+// GPU.
 template <int HD, bool MODS>
 lci_status launch_rows(const lci::AttnQ8Args& a, long long pairs, cudaStream_t st) {
-    const RowsShape sh = rows_q8_shape(a, pairs);
-    return sh.warps == 8 ? launch_attn_q8_rows<HD, 8, MODS>(a, pairs, sh.nsplit, st)
-                         : launch_attn_q8_rows<HD, 4, MODS>(a, pairs, sh.nsplit, st);
+    using Few = Q8Rows<HD, 8, MODS>;
+    using Many = Q8Rows<HD, 4, MODS>;
+    cudaError_t e = Few::prepare();
+    if (e == cudaSuccess) e = Many::prepare();
+    if (e != cudaSuccess) return fail(LCI_ERR_CUDA, "sparse_attn_q8: %s", cudaGetErrorString(e));
+    if (pairs <= 148) {
+        const int few = Few::best_split(a, pairs), many = Many::best_split(a, pairs);
+        if (2 * few >= many) return Few::launch(a, pairs, few, st);
+        return Many::launch(a, pairs, many, st);
+    }
+    return Many::launch(a, pairs, pairs <= 2 * 148 ? Many::best_split(a, pairs) : 1, st);
 }
 
 template <int IPT>
@@ -1645,18 +1705,11 @@ lci_status lci_block_weight_update(const int32_t* d_ids, const float* d_mass, in
     if (topk > lci::kMaxTopk || max_blocks > kMaxNbMax || batch > 65535)
         return fail(LCI_ERR_UNSUPPORTED, "block_weight_update: topk above %d, max_blocks above %d or "
                     "batch above 65535", lci::kMaxTopk, kMaxNbMax);
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(lci::block_weight_update_kernel,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        (int)lci::bwu::smem_bytes(lci::bwu::kMaxWarps));
-        if (attr_err == cudaSuccess)  // clusters of 16
-            attr_err = cudaFuncSetAttribute(lci::block_weight_update_kernel,
-                                            cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    });
-    if (attr_err != cudaSuccess)
-        return fail(LCI_ERR_CUDA, "block_weight_update: %s", cudaGetErrorString(attr_err));
+    static KernelSetup setup;
+    const cudaError_t se = setup.prepare(lci::block_weight_update_kernel,
+                                         (int)lci::bwu::smem_bytes(lci::bwu::kMaxWarps), true);
+    if (se != cudaSuccess)
+        return fail(LCI_ERR_CUDA, "block_weight_update: %s", cudaGetErrorString(se));
     // Rows are spread over warps, then over the CTAs of a cluster (while the
     // grid has room), until a warp has the few rows it loads at once.
     const int ranges = (max_blocks + lci::bwu::kRange - 1) / lci::bwu::kRange;
