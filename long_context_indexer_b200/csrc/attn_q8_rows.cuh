@@ -85,7 +85,7 @@ __device__ __forceinline__ VScale split_v_scale(float vs) {
     VScale r;
     r.f = __uint_as_float((u & 0x7fffffu) | 0x3f800000u);
     r.e = (float)e;
-    r.inv = __uint_as_float((uint32_t)(127 - e) << 23);
+    r.inv = __uint_as_float((uint32_t)max(127 - e, 1) << 23);
     return r;
 }
 

@@ -1,0 +1,742 @@
+// attn_q8_tile.cuh -- attention over the 8-bit paged cache for many queries per
+// sequence, on the 5th-generation tensor cores (tcgen05 + TMEM): bf16 queries,
+// head_dim 128, block_size a multiple of 64, up to 16 query heads per KV head.
+//
+// Tile. A CTA owns up to 128 MMA rows: QT = min(32, 128 / G) consecutive queries
+// of one sequence times the G query heads of one KV head. It walks the union of
+// the blocks its queries selected in units of 64 tokens, two units to a pair.
+//
+// The cached codes are never converted: K and V tiles come by TMA as they are
+// stored and are the 8-bit B operands of tcgen05.mma.kind::f8f6f4. The 16-bit
+// side is split instead. A bf16 query element, scaled by a power of two per row,
+// is the sum of two e4m3 numbers (4 + 4 significant bits, exact down to 2^-17 of
+// the row's largest element), and a softmax weight is rounded to such a sum (8
+// significant bits, the precision of a bf16 weight, down to 2^-15 of the row's
+// largest weight). Both products take two MMAs at twice the bf16 rate: the same
+// tensor time as a bf16 cache, half its shared-memory traffic, and no
+// conversion of 64 KiB per pair.
+//   S  = Qhi K^T + Qlo K^T   M=128, N=128 tokens, A = Q from TMEM
+//   O += Phi V   + Plo V     M=128, N=128 dims, K=64 tokens, A = P from TMEM,
+//                            B = V MN-major from shared memory
+//
+// Scales. A block's k scale multiplies the fp32 logits. With the v scale
+// f * 2^e, f in (1/2, 1], the weight of the codes is 2^(x + e - m) * f and the
+// row sum adds 2^(x - m), so the running reference m of a row is the maximum of
+// x + e. Weights are 2^5 at the reference; it moves only when a unit passes it
+// by more than 3.75 (weights stay below 448), and O is rescaled only then.
+//
+// Warps: 0 TMA producer, 1 MMA issuer, 2..5 and 6..9 two softmax groups that
+// take the even and the odd units, one thread per row. A warp (two queries at
+// 16 heads) none of whose queries selected the unit skips its loads and
+// exponentials, so with sparse selections the groups work ahead of each other
+// and the tensor pipe sets the pace (1028 cycles a pair). The groups agree on a
+// row's reference in unit order: a short chain of one mbarrier per 32 rows and
+// group, between the maximum and the exponentials of each unit.
+//
+// Unset memory and NaN. Units past the context, and V rows behind the last
+// token, never reach the MMA (skipped, or zeroed in shared memory). A NaN code
+// inside the context contaminates every row of the tile as 0 * NaN; rows whose
+// output holds a NaN are computed again by one warp each in fp32, which reads
+// only what the row attends.
+#pragma once
+
+#include "attn_prefill.cuh"
+#include "attn_q8_rows.cuh"
+#include "common.cuh"
+#include "index_prefill.cuh"
+#include "ptx.cuh"
+#include "q8_cache.cuh"
+
+namespace lci {
+
+namespace q8t {
+constexpr int kHD = 128;
+constexpr int kRows = 128;
+constexpr int kMaxQT = 32;             // queries per tile: a block's mask of them is a word
+constexpr int kUnit = 64;              // tokens per unit
+constexpr int kUnitBytes = kUnit * kHD;
+constexpr int kStageBytes = 2 * kUnitBytes;  // a pair: 16 KiB of K or of V
+constexpr int kStages = 4;
+constexpr int kMaxWords = 512;         // block bitmap words: nb_max <= 16384
+constexpr int kMaxUnion = 2048;        // distinct blocks per tile
+constexpr int kGroupWarps = 4;
+constexpr int kThreads = 64 + 2 * 32 * kGroupWarps;
+// TMEM columns: O fp32, two pairs of S (fp32; a unit's 64 columns then hold its
+// P as 16 columns of high and 16 of low parts), Q high and low parts
+constexpr int kColO = 0, kColS = 128, kColQ = 384, kTmemCols = 512;
+constexpr float kShift = 5.f;          // log2 of the weight at the reference
+constexpr float kLazy = 3.75f;         // 2^(5 + 3.75) < 448
+// shared memory (offsets from a 1024-byte aligned base)
+constexpr int kOffK = 0;
+constexpr int kOffV = kOffK + kStages * kStageBytes;
+constexpr int kOffUnion = kOffV + kStages * kStageBytes;
+constexpr int kUnionBytes = 2 * kMaxWords * 4 + 6 * kMaxUnion * 4;
+constexpr int kOffWin = kOffUnion + kUnionBytes;    // [kMaxQT] Q8Window
+constexpr int kOffBar = kOffWin + kMaxQT * 16;
+constexpr int kOffRow = kOffBar + 512;              // [128] references, [2][128] sums, [128] flags
+constexpr int kSmemBytes = kOffRow + 4 * 128 * 4 + 1024 /*alignment slack*/;
+// instruction descriptors, kind::f8f6f4: D fp32, A and B e4m3, M = 128, N = 128
+constexpr uint32_t kIdescQK = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);  // B MN-major
+}  // namespace q8t
+
+// D (+)= A B, 8-bit operands, A read from TMEM (4 elements per column).
+__device__ __forceinline__ void tc_mma_f8_tmem_a(uint32_t tmem_d, uint32_t tmem_a, uint64_t b,
+                                                 uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+
+// 2^e, e in -126 .. 127.
+__device__ __forceinline__ float exp2_int(int e) {
+    return __uint_as_float((uint32_t)(max(e, -126) + 127) << 23);
+}
+
+// f16x2 -> two e4m3 codes (low half first).
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 c;\n\tcvt.rn.satfinite.e4m3x2.f16x2 c, %1;\n\tcvt.u32.u16 %0, c;\n\t}" : "=r"(r) : "r"(h));
+    return r;
+}
+// Two non-negative weights -> the codes of their high and low parts.
+__device__ __forceinline__ void split_weights(float lo, float hi, uint32_t& h8, uint32_t& l8) {
+    const uint32_t p16 = pack_f16x2(lo, hi);
+    h8 = f16x2_to_e4m3x2(p16);
+    const uint32_t back = e4m3x2_to_f16x2(h8);
+    const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&p16), *reinterpret_cast<const __half2*>(&back));
+    l8 = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest));
+}
+
+// One query row and head by one warp, fp32, reading only attended tokens
+// (sq: hd floats of shared memory of this warp).
+__device__ __noinline__ void q8_row_by_warp(const AttnQ8Args& a, int row, int h, float* sq) {
+    constexpr int kPer = q8t::kHD / 32;
+    const int lane = threadIdx.x & 31;
+    const int b = row / a.S, s = row - b * a.S, g = h / (a.H_q / a.H_kv);
+    const __nv_bfloat16* qh = static_cast<const __nv_bfloat16*>(a.q) + ((size_t)row * a.H_q + h) * q8t::kHD;
+    __syncwarp();
+    for (int d = lane; d < q8t::kHD; d += 32) sq[d] = to_f32(qh[d]);
+    __syncwarp();
+    const Q8Window win = q8_window(a, row, b, s);
+    const float inv_cap = a.cap > 0.f ? 1.f / a.cap : 0.f, slope = a.slopes ? a.slopes[h] : 0.f;
+    float m = -INFINITY, l = 0.f, o[kPer] = {};
+    for (int i = 0; i < a.topk; ++i) {
+        const int j = a.ids[(size_t)row * a.topk + i];
+        const int page = q8_page(a, b, j, win);
+        if (page < 0) continue;
+        const size_t cell = (size_t)page * a.H_kv + g;
+        const float kmul = a.scale * a.ks[cell], vmul = a.vs[cell];
+        for (int u0 = 0; u0 < a.bs; u0 += 32) {
+            const int t = j * a.bs + u0 + lane;
+            const bool see = u0 + lane < a.bs && t >= win.lo && t <= win.hi;
+            float x = -INFINITY;
+            if (see) {
+                const uint8_t* kr = a.k + (cell * a.bs + u0 + lane) * q8t::kHD;
+                float dot = 0.f;
+                for (int d = 0; d < q8t::kHD; ++d) dot = fmaf(e4m3_to_f32(kr[d]), sq[d], dot);
+                x = q8_score(dot * kmul, a.cap, inv_cap, slope, abs(win.p - t));
+            }
+            const uint32_t seen = __ballot_sync(0xffffffffu, see);
+            if (seen == 0u) continue;
+            const float m_new = fmaxf(m, warp_max(x));
+            const float base = m_new == -INFINITY ? 0.f : m_new;
+            const float corr = exp2f(m - base), pw = exp2f(x - base);
+            m = m_new;
+            l = l * corr + warp_sum(pw);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) o[e] *= corr;
+            for (uint32_t left = seen; left != 0u; left &= left - 1u) {
+                const int t1 = __ffs(left) - 1;
+                const float p1 = __shfl_sync(0xffffffffu, pw, t1) * vmul;
+                const uint8_t* vr = a.v + (cell * a.bs + u0 + t1) * q8t::kHD + lane;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) o[e] = fmaf(p1, e4m3_to_f32(vr[32 * e]), o[e]);
+            }
+        }
+    }
+    __nv_bfloat16* oh = static_cast<__nv_bfloat16*>(a.out) + ((size_t)row * a.H_q + h) * q8t::kHD;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) oh[lane + 32 * e] = __float2bfloat16_rn(l == 0.f ? 0.f : o[e] / l);
+    if (a.lse && lane == 0) a.lse[(size_t)row * a.H_q + h] = l == 0.f ? -INFINITY : m + log2f(l);
+}
+
+template <bool MODS>
+__global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
+    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+    const __grid_constant__ AttnQ8Args a, int batch, int q_tiles) {
+    using namespace q8t;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint32_t* bitmap = reinterpret_cast<uint32_t*>(smem + kOffUnion);  // [kMaxWords]
+    uint32_t* wpre = bitmap + kMaxWords;                               // [kMaxWords]
+    int* ublk = reinterpret_cast<int*>(wpre + kMaxWords);              // [kMaxUnion] block
+    int* upage = ublk + kMaxUnion;                                     // page, or -1
+    uint32_t* umask = reinterpret_cast<uint32_t*>(upage + kMaxUnion);  // queries that selected it
+    float* uks = reinterpret_cast<float*>(umask + kMaxUnion);          // k scale
+    float* uve = uks + kMaxUnion;                                      // v scale = uvf * 2^uve
+    float* uvf = uve + kMaxUnion;
+    Q8Window* wins = reinterpret_cast<Q8Window*>(smem + kOffWin);      // [kMaxQT]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
+    uint64_t* kfull = bars;                // [kStages]
+    uint64_t* kempty = kfull + kStages;    // [kStages]
+    uint64_t* vfull = kempty + kStages;    // [kStages]
+    uint64_t* vempty = vfull + kStages;    // [kStages]
+    uint64_t* sfull = vempty + kStages;    // [2] a pair's S written
+    uint64_t* pfull = sfull + 2;           // [4] a unit's P written (4 warps)
+    uint64_t* decided = pfull + 4;         // [2][4] a group's reference of a unit, per 32 rows
+    uint64_t* obar = decided + 8;          // [4] a unit's P V completed
+    uint64_t* drain = obar + 4;            // every MMA of the tile completed
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    int* s_nunion = reinterpret_cast<int*>(tmem_slot + 1);
+    // set by any role whose bounded wait ran out: every role then stops
+    volatile int* s_abort = s_nunion + 1;
+    static_assert((4 * kStages + 2 + 4 + 8 + 4 + 1) * 8 + 12 <= 512, "barriers fit");
+    float* mref = reinterpret_cast<float*>(smem + kOffRow);  // [128]
+    float* lsum = mref + 128;                                // [2][128]
+    int* redo = reinterpret_cast<int*>(lsum + 256);          // [128]
+
+    pdl_wait();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = a.H_q / a.H_kv;
+    const int QT = min(kMaxQT, kRows / G);
+    // the latest queries (most visible blocks) of every sequence first
+    const int per_qt = batch * a.H_kv;
+    const int qt = q_tiles - 1 - (int)(blockIdx.x / per_qt);
+    const int rest = (int)(blockIdx.x % per_qt);
+    const int b = rest / a.H_kv, g = rest - b * a.H_kv;
+    const int s0 = qt * QT;
+    const int nwords = (a.nb_max + 31) >> 5;
+    const int upb = a.bs / kUnit;  // units per block
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&kfull[i], 1);
+            mbar_init(&kempty[i], 1);
+            mbar_init(&vfull[i], 1);
+            mbar_init(&vempty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) mbar_init(&sfull[i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&pfull[i], kGroupWarps);
+        for (int i = 0; i < 8; ++i) mbar_init(&decided[i], 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&obar[i], 1);
+        mbar_init(drain, 1);
+        *s_abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(tmem_slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+    }
+    // ---------------- the union of the tile's selected blocks ----------------
+    const int nent = QT * a.topk;
+    for (int w = tid; w < nwords; w += kThreads) bitmap[w] = 0u;
+    for (int e = tid; e < min(nent, kMaxUnion); e += kThreads) umask[e] = 0u;
+    if (tid < kMaxQT) {
+        Q8Window w{0, -1, 0};
+        if (tid < QT && s0 + tid < a.S) w = q8_window(a, b * a.S + s0 + tid, b, s0 + tid);
+        wins[tid] = w;
+    }
+    if (tid < kRows) {
+        mref[tid] = -INFINITY;
+        redo[tid] = 0;
+    }
+    __syncthreads();
+    // block of entry e if its query can attend a token of it, else -1
+    auto entry = [&](int e, int& qi) -> int {
+        qi = e / a.topk;
+        if (s0 + qi >= a.S) return -1;
+        const int j = __ldg(a.ids + ((size_t)b * a.S + s0) * a.topk + e);
+        if (j < 0 || j >= a.nb_max) {
+            if (j != -1) raise_status(kStatusBadBlockId);
+            return -1;
+        }
+        const int first = j * a.bs;
+        return first <= wins[qi].hi && first + a.bs > wins[qi].lo ? j : -1;
+    };
+    for (int e = tid; e < nent; e += kThreads) {
+        int qi;
+        const int j = entry(e, qi);
+        if (j >= 0) atomicOr(&bitmap[j >> 5], 1u << (j & 31));
+    }
+    __syncthreads();
+    if (warp == 0) {  // exclusive prefix of the words' population counts
+        const int per = (nwords + 31) / 32;
+        int sum = 0;
+        for (int k = 0; k < per; ++k) {
+            const int w = lane * per + k;
+            if (w < nwords) sum += __popc(bitmap[w]);
+        }
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int t = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += t;
+        }
+        int run = incl - sum;
+        for (int k = 0; k < per; ++k) {
+            const int w = lane * per + k;
+            if (w < nwords) {
+                wpre[w] = (uint32_t)run;
+                run += __popc(bitmap[w]);
+            }
+        }
+        if (lane == 31) *s_nunion = incl;
+    }
+    __syncthreads();
+    for (int e = tid; e < nent; e += kThreads) {
+        int qi;
+        const int j = entry(e, qi);
+        if (j >= 0) {
+            const int pos = (int)wpre[j >> 5] + __popc(bitmap[j >> 5] & ((1u << (j & 31)) - 1u));
+            ublk[pos] = j;
+            atomicOr(&umask[pos], 1u << qi);
+        }
+    }
+    __syncthreads();
+    const int nunion = *s_nunion;
+    for (int u = tid; u < nunion; u += kThreads) {
+        int page = a.table[(size_t)b * a.nb_max + ublk[u]];
+        if (page < 0 || page >= a.num_pages) {
+            raise_status(kStatusBadPage);
+            page = -1;
+        }
+        upage[u] = page;
+        const size_t cell = page >= 0 ? (size_t)page * a.H_kv + g : 0;
+        uks[u] = page >= 0 ? a.ks[cell] : 0.f;
+        // f in (1/2, 1]: f * 2^e with the weight of the codes at most 2^(x + e - m)
+        const float vs = page >= 0 ? fmaxf(a.vs[cell], kMinVScale) : 1.f;
+        const uint32_t bits = __float_as_uint(vs);
+        const bool pow2 = (bits & 0x7fffffu) == 0u;
+        uve[u] = (float)((int)(bits >> 23) - (pow2 ? 127 : 126));
+        uvf[u] = pow2 ? 1.f : __uint_as_float((bits & 0x7fffffu) | 0x3f000000u);
+    }
+    const int nunits = nunion * upb;
+    const int npairs = (nunits + 1) / 2;
+    const long long ctx = a.ctx_len[b];
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    // named barrier 1: the MMA warp waits for the query rows in TMEM;
+    // named barrier 2: the softmax warps before the epilogue
+    constexpr int kQBarrier = 1, kQThreads = 32 + 64 * kGroupWarps;
+    constexpr int kEndBarrier = 2, kEndThreads = 64 * kGroupWarps;
+
+    int issued = 0;  // pairs whose copies the producer thread started
+    if (warp == 0) {
+        // ---------------- TMA producer ----------------
+        if (lane == 0) {
+            for (int i = 0; i < npairs; ++i) {
+                const int st = i % kStages;
+                const uint32_t ph = ((i / kStages) - 1) & 1;
+                int ys[2], nload = 0;
+                for (int c = 0; c < 2; ++c) {
+                    const int u = 2 * i + c;
+                    ys[c] = -1;
+                    if (u < nunits) {
+                        const int blk = u / upb, sub = u - blk * upb;
+                        const int page = upage[blk];
+                        if (page >= 0) {
+                            ys[c] = (page * a.H_kv + g) * a.bs + sub * kUnit;
+                            ++nload;
+                        }
+                    }
+                }
+                bool ok = true;
+                issued = i + 1;
+                for (int kv = 0; kv < 2 && ok; ++kv) {
+                    uint64_t* full = kv ? &vfull[st] : &kfull[st];
+                    if (*s_abort || (i >= kStages && !mbar_wait(kv ? &vempty[st] : &kempty[st], ph))) {
+                        *s_abort = 1;
+                        ok = false;
+                        break;
+                    }
+                    unsigned char* dst = smem + (kv ? kOffV : kOffK) + st * kStageBytes;
+                    if (nload) {
+                        mbar_arrive_expect_tx(full, (uint32_t)nload * kUnitBytes);
+                        for (int c = 0; c < 2; ++c)
+                            if (ys[c] >= 0) tma_load_2d(dst + c * kUnitBytes, kv ? &tm_v : &tm_k, 0, ys[c], full);
+                    } else {
+                        mbar_arrive(full);
+                    }
+                }
+                if (!ok) break;
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        named_barrier_sync(kQBarrier, kQThreads);
+        tc_fence_after();
+        if (lane == 0) {
+            uint32_t any_pv = 0u;  // O holds something
+            auto pv = [&](int j) -> bool {
+                const int vs = j % kStages;
+                const uint32_t vb = smem_u32(smem + kOffV + vs * kStageBytes);
+                for (int c = 0; c < 2; ++c) {
+                    const int u = 2 * j + c;
+                    if (!mbar_wait(&pfull[u & 3], (u >> 2) & 1) ||
+                        !mbar_wait(&vfull[vs], (j / kStages) & 1)) {
+                        *s_abort = 1;
+                        return false;
+                    }
+                    tc_fence_after();
+                    if (u < nunits && upage[u / upb] >= 0) {
+                        const uint32_t p = tmem_base + kColS + (u & 3) * 64;
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+#pragma unroll
+                            for (int kt = 0; kt < kUnit / 32; ++kt) {
+                                tc_mma_f8_tmem_a(tmem_base + kColO, p + part * 16 + kt * 8,
+                                                 sw128_desc_mn(vb + c * kUnitBytes + kt * 4096, kUnitBytes),
+                                                 kIdescPV, any_pv);
+                                any_pv = 1u;
+                            }
+                    }
+                    tc_commit(&obar[u & 3]);
+                }
+                tc_commit(&vempty[vs]);
+                return true;
+            };
+            bool fine = true;
+            for (int i = 0; i < npairs && fine; ++i) {
+                const int ks = i % kStages;
+                if (*s_abort || !mbar_wait(&kfull[ks], (i / kStages) & 1)) {
+                    *s_abort = 1;
+                    fine = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t kb = smem_u32(smem + kOffK + ks * kStageBytes);
+                const uint32_t d = tmem_base + kColS + (i & 1) * 128;
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int kk = 0; kk < kHD / 32; ++kk)
+                        tc_mma_f8_tmem_a(d, tmem_base + kColQ + part * 32 + kk * 8, sw128_desc(kb) + 2 * kk,
+                                         kIdescQK, (part | kk) != 0 ? 1u : 0u);
+                tc_commit(&kempty[ks]);
+                tc_commit(&sfull[i & 1]);
+                if (i > 0) fine = pv(i - 1);
+            }
+            if (fine && npairs > 0) pv(npairs - 1);
+            // nothing of this thread may still run on the tensor core when the
+            // TMEM is released; the epilogue waits for it too
+            tc_commit(drain);
+            mbar_wait(drain, 0);
+        }
+    } else {
+        // ---------------- softmax and epilogue: a thread per row and group ----------------
+        const int grp = (warp - 2) >> 2;  // units 2i + grp
+        const int quarter = warp & 3;     // TMEM lanes of this warp
+        const int r = quarter * 32 + lane;
+        const int qi = r / G, s = s0 + qi;
+        const bool real = qi < QT && s < a.S;
+        const int h = g * G + (r - qi * G);
+        const size_t qrow = ((size_t)b * a.S + s) * a.H_q + h;
+        const uint32_t qbit = real ? 1u << qi : 0u;
+        const Q8Window win = wins[min(qi, kMaxQT - 1)];
+        const uint32_t lane_addr = tmem_base + ((uint32_t)(quarter * 32) << 16);
+        const int ctx32 = (int)(ctx < 0x7fffffffLL ? ctx : 0x7fffffffLL);
+        float unit = MODS ? a.scale : a.scale * kLog2e;  // what raw S is multiplied by, with the k scale
+        // ---- query row -> TMEM: group 0 stores the high parts, group 1 the low ----
+        {
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + qrow * kHD);
+            uint4 w[16];
+            float amax = 0.f;
+            bool odd = false;  // not finite
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                w[c] = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = bf16x2_to_f32(x[k]);
+                    amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    odd = odd || f.x != f.x || f.y != f.y;
+                }
+            }
+            odd = odd || amax > 3.402823466e38f;
+            if (odd) redo[r] = 1;  // such a row is computed apart
+            int e = (int)(__float_as_uint(amax) >> 23) - 127;
+            e = e < -100 ? -100 : e > 127 ? 127 : e;
+            const float up = __uint_as_float((uint32_t)(7 - e + 127) << 23);  // largest element in [2^7, 2^8)
+            unit *= __uint_as_float((uint32_t)(e - 7 + 127) << 23);
+            uint32_t part[32];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float2 f0 = bf16x2_to_f32(x[2 * k]), f1 = bf16x2_to_f32(x[2 * k + 1]);
+                    f0.x *= up;
+                    f0.y *= up;
+                    f1.x *= up;
+                    f1.y *= up;
+                    const uint32_t h0 = f32_to_e4m3x2(f0.x, f0.y), h1 = f32_to_e4m3x2(f1.x, f1.y);
+                    uint32_t word = h0 | (h1 << 16);
+                    if (grp == 1) {
+                        const float2 b0 = f16x2_to_f32(e4m3x2_to_f16x2(h0)), b1 = f16x2_to_f32(e4m3x2_to_f16x2(h1));
+                        word = f32_to_e4m3x4(f0.x - b0.x, f0.y - b0.y, f1.x - b1.x, f1.y - b1.y);
+                    }
+                    part[2 * c + k] = word;
+                }
+            }
+            tmem_st32(lane_addr + kColQ + grp * 32, part);
+            tmem_wait_st();
+            tc_fence_before();
+            named_barrier_sync(kQBarrier, kQThreads);
+        }
+        float slope2 = 0.f, cap2 = 0.f, inv_cap = 0.f;
+        if constexpr (MODS) {
+            if (a.slopes && real) slope2 = a.slopes[h] * kLog2e;
+            if (a.cap > 0.f) {
+                inv_cap = 1.f / a.cap;
+                cap2 = a.cap * kLog2e;
+            }
+        }
+        float m = -INFINITY;  // the row's reference, in step with the other group's
+        float l = 0.f;        // this group's share of the row sum, relative to m
+        uint64_t* my_dec = decided + grp * 4 + quarter;
+        uint64_t* their_dec = decided + (grp ^ 1) * 4 + quarter;
+        bool stop = false;
+        for (int i = 0; i < npairs; ++i) {
+            const int u = 2 * i + grp;
+            // the unit: its block's entry, first token, and what the row sees of it
+            const int blk = u < nunits ? u / upb : 0;
+            const int page = u < nunits ? upage[blk] : -1;
+            const uint32_t mask = umask[blk];
+            const int t0 = ublk[blk] * a.bs + (u - blk * upb) * kUnit;
+            int lo = 0, hi = -1;  // attended columns lo .. hi
+            if (page >= 0 && (mask & qbit) != 0u) {
+                lo = max(win.lo - t0, 0);
+                hi = min(win.hi - t0, kUnit - 1);
+            }
+            const bool mine = hi >= lo;
+            const bool warp_any = __any_sync(0xffffffffu, mine);
+            const float ks = uks[blk], ve = uve[blk], vf = uvf[blk];
+            const uint32_t scol = lane_addr + kColS + (u & 3) * 64;
+            if (!mbar_wait(&sfull[i & 1], (i >> 1) & 1)) {
+                *s_abort = 1;
+                stop = true;
+            }
+            if (*s_abort) stop = true;
+            stop = __any_sync(0xffffffffu, stop);
+            tc_fence_after();
+            float mx = -INFINITY;
+            float mul = unit * ks;
+            uint32_t sv[64];
+            if (warp_any && !stop) {
+                tmem_ld64(scol, sv);
+                if constexpr (MODS) {
+                    // raw S -> capped, biased logits in log2 units; then mul = 1
+                    float xs[64];
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) xs[e] = __uint_as_float(sv[e]);
+                    if (a.cap > 0.f) {
+                        const float um = mul * inv_cap;
+                        float big = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) big = fmaxf(big, fabsf(xs[e]));
+                        if (__any_sync(0xffffffffu, mine && !(big * fabsf(um) <= kTanhSmall))) {
+#pragma unroll
+                            for (int e = 0; e < 64; ++e) xs[e] = cap2 * q8_tanh(xs[e] * um);
+                        } else {
+                            // every |u| is small: the polynomial on packed pairs
+                            const float2 um2 = make_float2(um, um), c2 = make_float2(cap2, cap2);
+                            const float2 z2 = make_float2(0.f, 0.f);
+#pragma unroll
+                            for (int e = 0; e < 64; e += 2) {
+                                const float2 x = ffma2(make_float2(xs[e], xs[e + 1]), um2, z2);
+                                const float2 v = ffma2(x, x, z2);
+                                float2 p = ffma2(v, make_float2(kTanhC4, kTanhC4), make_float2(kTanhC3, kTanhC3));
+                                p = ffma2(v, p, make_float2(kTanhC2, kTanhC2));
+                                p = ffma2(v, p, make_float2(kTanhC1, kTanhC1));
+                                p = ffma2(v, p, make_float2(kTanhC0, kTanhC0));
+                                const float2 t = ffma2(ffma2(x, v, z2), p, x);
+                                const float2 y = ffma2(t, c2, z2);
+                                xs[e] = y.x;
+                                xs[e + 1] = y.y;
+                            }
+                        }
+                    } else {
+                        const float m2 = mul * kLog2e;
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) xs[e] *= m2;
+                    }
+                    if (a.slopes) {
+                        const float d0 = (float)(win.p - t0);
+#pragma unroll
+                        for (int e = 0; e < 64; ++e) xs[e] = fmaf(-slope2, fabsf(d0 - (float)e), xs[e]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) sv[e] = __float_as_uint(xs[e]);
+                    mul = 1.f;
+                }
+                if (hi - lo != kUnit - 1) {
+#pragma unroll
+                    for (int e = 0; e < 64; ++e)
+                        sv[e] = e >= lo && e <= hi ? sv[e] : __float_as_uint(-INFINITY);
+                }
+                float pm[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) pm[k] = __uint_as_float(sv[k]);
+#pragma unroll
+                for (int e = 8; e < 64; e += 2)
+                    pm[(e >> 1) & 7] = fmax3(pm[(e >> 1) & 7], __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
+                mx = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
+                mx = mx * mul + ve;
+            }
+            // the reference after the unit before this one, then after this one
+            if (grp == 1 || i > 0) {
+                if (!stop && !mbar_wait(their_dec, grp == 1 ? i & 1 : (i - 1) & 1)) {
+                    *s_abort = 1;
+                    stop = true;
+                }
+                stop = __any_sync(0xffffffffu, stop);
+            }
+            if (stop) break;
+            const float m_in = mref[r];
+            if (m_in != m) {
+                l *= fast_exp2(m - m_in);  // m = -inf: nothing summed yet
+                m = m_in;
+            }
+            float corr = 1.f;
+            if (mx > m + kLazy) {
+                if (m > -INFINITY) corr = fast_exp2(m - mx);
+                l *= corr;
+                m = mx;
+                mref[r] = m;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(my_dec);
+            uint32_t pk[32];  // 16 words of high parts, 16 of low parts
+            if (mine) {
+                const float add = ve + kShift - m;
+                const float2 mul2 = make_float2(mul, mul), add2 = make_float2(add, add);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    uint32_t hi8[2], lo8[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float2 x = ffma2(make_float2(__uint_as_float(sv[4 * e + 2 * k]),
+                                                           __uint_as_float(sv[4 * e + 2 * k + 1])), mul2, add2);
+                        float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                        sum[k] = fadd2(sum[k], p);
+                        if (vf != 1.f) {
+                            p.x *= vf;
+                            p.y *= vf;
+                        }
+                        split_weights(p.x, p.y, hi8[k], lo8[k]);
+                    }
+                    pk[e] = __byte_perm(hi8[0], hi8[1], 0x5410);
+                    pk[16 + e] = __byte_perm(lo8[0], lo8[1], 0x5410);
+                }
+                const float2 t = fadd2(sum[0], sum[1]);
+                l = fmaf(t.x + t.y, exp2_int(-(int)ve), l);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) pk[e] = 0u;
+            }
+            tmem_st32(scol, pk);
+            if (__any_sync(0xffffffffu, corr != 1.f)) {
+                // O holds earlier units of these rows: rescale once the previous
+                // unit's P V has landed
+                if (!mbar_wait(&obar[(u - 1) & 3], ((u - 1) >> 2) & 1)) *s_abort = 1;
+                tc_fence_after();
+#pragma unroll 1
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t ov[32];
+                    tmem_ld32(lane_addr + kColO + ch * 32, ov);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * corr);
+                    tmem_st32(lane_addr + kColO + ch * 32, ov);
+                }
+            }
+            tmem_wait_st();
+            // V rows of tokens past the context must be zero before the MMA
+            // reads them (this thread: half of row r / 2 of the unit)
+            if (page >= 0 && t0 > ctx32 - kUnit) {
+                const int vs = i % kStages;
+                if (!mbar_wait(&vfull[vs], (i / kStages) & 1)) *s_abort = 1;
+                const int vr = r >> 1;
+                if (t0 + vr >= ctx32) {
+                    unsigned char* vt = smem + kOffV + vs * kStageBytes + grp * kUnitBytes + vr * 128;
+#pragma unroll
+                    for (int c = 4 * (r & 1); c < 4 * (r & 1) + 4; ++c)
+                        *reinterpret_cast<uint4*>(vt + ((c ^ (vr & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pfull[u & 3]);
+        }
+        // ---------------- epilogue: O / l -> bf16, 64 dims per group ----------------
+        named_barrier_sync(kEndBarrier, kEndThreads);  // both groups' references are final
+        const float m_end = mref[r];
+        if (m_end != m) l *= fast_exp2(m - m_end);
+        lsum[grp * 128 + r] = l;
+        named_barrier_sync(kEndBarrier, kEndThreads);
+        const float L = lsum[r] + lsum[128 + r];
+        if (!mbar_wait(drain, 0)) *s_abort = 1;
+        tc_fence_after();
+        const float inv = 1.f / L;
+        if (a.lse && real && grp == 0) a.lse[qrow] = L == 0.f ? -INFINITY : m_end - kShift + log2f(L);
+        __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) + qrow * kHD + grp * 64;
+        bool bad = false;
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+            uint32_t ov[32];
+            tmem_ld32(lane_addr + kColO + grp * 64 + ch * 32, ov);
+            if (real) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    // a row that attends nothing is zero whatever O holds
+                    const float x = L == 0.f ? 0.f : __uint_as_float(ov[2 * e]) * inv;
+                    const float y = L == 0.f ? 0.f : __uint_as_float(ov[2 * e + 1]) * inv;
+                    bad = bad || x != x || y != y;
+                    w[e] = pack_bf16x2(x, y);
+                }
+                uint4* dst = reinterpret_cast<uint4*>(orow + ch * 32);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            }
+        }
+        if (bad) redo[r] = 1;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                     "r"(kTmemCols)
+                     : "memory");
+    }
+    // a tile that gave up: its copies still land before the CTA's memory is reused
+    if (*s_abort && tid == 0)
+        for (int i = max(0, issued - kStages); i < issued; ++i) {
+            mbar_wait(&kfull[i % kStages], (i / kStages) & 1);
+            mbar_wait(&vfull[i % kStages], (i / kStages) & 1);
+        }
+    // rows that met a NaN (the K ring is free: every copy was consumed)
+    if (!*s_abort)
+        for (int r = warp; r < QT * G; r += kThreads / 32)
+            if (redo[r] && s0 + r / G < a.S)
+                q8_row_by_warp(a, b * a.S + s0 + r / G, g * G + r % G,
+                               reinterpret_cast<float*>(smem + kOffK) + warp * kHD);
+}
+
+}  // namespace lci

@@ -19,6 +19,7 @@
 #include "attn_prefill.cuh"
 #include "attn_q8_rows.cuh"
 #include "attn_q8_simt.cuh"
+#include "attn_q8_tile.cuh"
 #include "attn_simt.cuh"
 #include "cache_evict.cuh"
 #include "common.cuh"
@@ -1569,6 +1570,78 @@ lci_status launch_rows(const lci::AttnQ8Args& a, long long pairs, cudaStream_t s
     return Many::launch(a, pairs, pairs <= 2 * 148 ? Many::best_split(a, pairs) : 1, st);
 }
 
+// The tile schedule (attn_q8_tile.cuh).
+int tile_q8_queries(const lci::AttnQ8Args& a) {
+    return std::min(lci::q8t::kMaxQT, lci::q8t::kRows / (a.H_q / a.H_kv));
+}
+bool tile_q8_fits(const lci::AttnQ8Args& a, lci_dtype dtype, const lci_block_table* t) {
+    return dtype == LCI_BF16 && a.hd == lci::q8t::kHD && a.bs % lci::q8t::kUnit == 0 && !a.mass &&
+           a.H_q / a.H_kv <= 16 && a.nb_max <= 32 * lci::q8t::kMaxWords &&
+           std::min<long long>((long long)tile_q8_queries(a) * a.topk, a.nb_max) <=
+               lci::q8t::kMaxUnion &&
+           (long long)t->num_pages * a.H_kv * a.bs < (1ll << 31);
+}
+
+// 8-bit pools [P][H_kv][bs][128] as rows of 128 bytes, read in boxes of 64 rows
+// with the 128-byte swizzle.
+lci_status q8_pool_maps(const lci_block_table* t, const void* k_pool, const void* v_pool,
+                        CUtensorMap* tm_k, CUtensorMap* tm_v) {
+    lci_block_table* mt = const_cast<lci_block_table*>(t);
+    std::lock_guard<std::mutex> lock(mt->map_mu);
+    if (mt->map_k_pool != k_pool || mt->map_v_pool != v_pool) {
+        auto enc = tensor_map_encoder();
+        if (!enc) return fail(LCI_ERR_CUDA, "sparse_attn_q8: cuTensorMapEncodeTiled unavailable");
+        cuuint64_t dims[2] = {128, (cuuint64_t)t->num_pages * t->num_kv_heads * t->block_size};
+        cuuint64_t strides[1] = {128};
+        cuuint32_t box[2] = {128, 64}, estr[2] = {1, 1};
+        mt->map_k_pool = mt->map_v_pool = nullptr;
+        for (int kv = 0; kv < 2; ++kv) {
+            const CUresult r = enc(kv ? &mt->map_v : &mt->map_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                                   const_cast<void*>(kv ? v_pool : k_pool), dims, strides, box, estr,
+                                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+            if (r != CUDA_SUCCESS)
+                return fail(LCI_ERR_CUDA, "sparse_attn_q8: tensor map encode failed (%d)", (int)r);
+        }
+        mt->map_k_pool = k_pool;
+        mt->map_v_pool = v_pool;
+    }
+    *tm_k = mt->map_k;
+    *tm_v = mt->map_v;
+    return LCI_OK;
+}
+
+template <bool MODS>
+lci_status launch_tile(const lci::AttnQ8Args& a, int32_t batch, const lci_block_table* t,
+                       cudaStream_t st) {
+    static KernelSetup setup;
+    CUtensorMap tm_k, tm_v;
+    const lci_status s = q8_pool_maps(t, a.k, a.v, &tm_k, &tm_v);
+    if (s != LCI_OK) return s;
+    auto kern = lci::sparse_attn_q8_tile_kernel<MODS>;
+    cudaError_t e = setup.prepare(kern, lci::q8t::kSmemBytes);
+    const int QT = tile_q8_queries(a), q_tiles = (a.S + QT - 1) / QT;
+    const long long tiles = (long long)batch * q_tiles * a.H_kv;
+    if (tiles >= (1ll << 31)) return fail(LCI_ERR_UNSUPPORTED, "sparse_attn_q8: grid too large");
+    if (e == cudaSuccess)
+        e = launch_early(kern, dim3((unsigned)tiles), dim3(lci::q8t::kThreads), lci::q8t::kSmemBytes, st,
+                         1, tm_k, tm_v, a, batch, q_tiles);
+    if (e != cudaSuccess) return fail(LCI_ERR_CUDA, "sparse_attn_q8: %s", cudaGetErrorString(e));
+    return check_launch("sparse_attn_q8");
+}
+
+// Which schedule a call takes: the tile schedule when asked for and it fits,
+// or, left to choose, for many queries per sequence whose selections are likely
+// to share blocks (at most four times as many blocks as a tile's queries select
+// in all); otherwise the row-wise one.
+bool use_tile_q8(const lci::AttnQ8Args& a, lci_dtype dtype, const lci_block_table* t,
+                 lci_phase phase) {
+    if (phase == LCI_PHASE_DECODE || !tile_q8_fits(a, dtype, t)) return false;
+    if (phase == LCI_PHASE_PREFILL) return true;
+    return a.S >= 16 && (long long)a.nb_max <= 4ll * tile_q8_queries(a) * a.topk;
+}
+
 template <int IPT>
 cudaError_t launch_evict(const lci_block_table* t, int32_t batch, const int32_t* ctx_len,
                          const float* weight, int32_t budget, int32_t sink, int32_t recent,
@@ -1683,9 +1756,11 @@ lci_status lci_sparse_attn_q8(const void* q, lci_dtype dtype, int32_t batch, int
     a.lse = d_lse;
     a.mass = d_mass;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const bool mods = a.cap > 0.f || a.slopes;
+    if (use_tile_q8(a, dtype, table, phase))
+        return mods ? launch_tile<true>(a, batch, table, cs) : launch_tile<false>(a, batch, table, cs);
     const long long pairs = (long long)batch * S * a.H_kv;
     if (rows_q8_fits(a, dtype) && pairs < (1ll << 27)) {
-        const bool mods = a.cap > 0.f || a.slopes;
         if (a.hd == 128) return mods ? launch_rows<128, true>(a, pairs, cs) : launch_rows<128, false>(a, pairs, cs);
         return mods ? launch_rows<64, true>(a, pairs, cs) : launch_rows<64, false>(a, pairs, cs);
     }
