@@ -347,8 +347,9 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const uint32_t w[4] = {cur.k[j][c].x, cur.k[j][c].y, cur.k[j][c].z, cur.k[j][c].w};
-                    mma_f16_16816(k & 1 ? sd[j] : sc[j], qf[4 * c + k], e4m3x2_to_f16x2(w[k]),
-                                  e4m3x2_to_f16x2(w[k] >> 16));
+                    uint32_t b0, b1;
+                    e4m3x4_to_f16(w[k], b0, b1);
+                    mma_f16_16816(k & 1 ? sd[j] : sc[j], qf[4 * c + k], b0, b1);
                 }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -432,14 +433,16 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
         // O += P V
 #pragma unroll
         for (int w = 0; w < HD / 32; ++w) {
-            const uint32_t ab0 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x5140);
-            const uint32_t ab1 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x7362);
-            const uint32_t cd0 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x5140);
-            const uint32_t cd1 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x7362);
-            mma_f16_16816(o[4 * w], pf, e4m3x2_to_f16x2(ab0), e4m3x2_to_f16x2(cd0));
-            mma_f16_16816(o[4 * w + 1], pf, e4m3x2_to_f16x2(ab0 >> 16), e4m3x2_to_f16x2(cd0 >> 16));
-            mma_f16_16816(o[4 * w + 2], pf, e4m3x2_to_f16x2(ab1), e4m3x2_to_f16x2(cd1));
-            mma_f16_16816(o[4 * w + 3], pf, e4m3x2_to_f16x2(ab1 >> 16), e4m3x2_to_f16x2(cd1 >> 16));
+            // bytes of tokens (2q, 2q+1) and (2q+8, 2q+9) paired: dims 4w .. 4w+3
+            uint32_t x0, x1, x2, x3, y0, y1, y2, y3;
+            e4m3x4_to_f16(__byte_perm(cur.v[0][w], cur.v[1][w], 0x5140), x0, x1);
+            e4m3x4_to_f16(__byte_perm(cur.v[0][w], cur.v[1][w], 0x7362), x2, x3);
+            e4m3x4_to_f16(__byte_perm(cur.v[2][w], cur.v[3][w], 0x5140), y0, y1);
+            e4m3x4_to_f16(__byte_perm(cur.v[2][w], cur.v[3][w], 0x7362), y2, y3);
+            mma_f16_16816(o[4 * w], pf, x0, y0);
+            mma_f16_16816(o[4 * w + 1], pf, x1, y1);
+            mma_f16_16816(o[4 * w + 2], pf, x2, y2);
+            mma_f16_16816(o[4 * w + 3], pf, x3, y3);
         }
         if (!more || n_blk != c_blk) close_block(c_blk);
         have = more;

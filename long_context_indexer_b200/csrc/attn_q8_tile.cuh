@@ -56,7 +56,7 @@ constexpr int kMaxQT = 32;             // queries per tile: a block's mask of th
 constexpr int kUnit = 64;              // tokens per unit
 constexpr int kUnitBytes = kUnit * kHD;
 constexpr int kStageBytes = 2 * kUnitBytes;  // a pair: 16 KiB of K or of V
-constexpr int kStages = 4;
+constexpr int kStages = 4;             // a power of two
 constexpr int kMaxWords = 512;         // block bitmap words: nb_max <= 16384
 constexpr int kMaxUnion = 2048;        // distinct blocks per tile
 constexpr int kGroupWarps = 4;
@@ -70,7 +70,7 @@ constexpr float kLazy = 3.75f;         // 2^(5 + 3.75) < 448
 constexpr int kOffK = 0;
 constexpr int kOffV = kOffK + kStages * kStageBytes;
 constexpr int kOffUnion = kOffV + kStages * kStageBytes;
-constexpr int kUnionBytes = 2 * kMaxWords * 4 + 6 * kMaxUnion * 4;
+constexpr int kUnionBytes = 2 * kMaxWords * 4 + kMaxUnion * (16 + 4);
 constexpr int kOffWin = kOffUnion + kUnionBytes;    // [kMaxQT] Q8Window
 constexpr int kOffBar = kOffWin + kMaxQT * 16;
 constexpr int kOffRow = kOffBar + 512;              // [128] references, [2][128] sums, [128] flags
@@ -94,19 +94,26 @@ __device__ __forceinline__ float exp2_int(int e) {
     return __uint_as_float((uint32_t)(max(e, -126) + 127) << 23);
 }
 
-// f16x2 -> two e4m3 codes (low half first).
-__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h) {
+// Two f16x2 -> four e4m3 codes.
+__device__ __forceinline__ uint32_t f16x4_to_e4m3(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("{\n\t.reg .b16 c;\n\tcvt.rn.satfinite.e4m3x2.f16x2 c, %1;\n\tcvt.u32.u16 %0, c;\n\t}" : "=r"(r) : "r"(h));
+    asm("{\n\t.reg .b16 s, t;\n\tcvt.rn.satfinite.e4m3x2.f16x2 s, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f16x2 t, %2;\n\tmov.b32 %0, {s, t};\n\t}"
+        : "=r"(r)
+        : "r"(a), "r"(b));
     return r;
 }
-// Two non-negative weights -> the codes of their high and low parts.
-__device__ __forceinline__ void split_weights(float lo, float hi, uint32_t& h8, uint32_t& l8) {
-    const uint32_t p16 = pack_f16x2(lo, hi);
-    h8 = f16x2_to_e4m3x2(p16);
-    const uint32_t back = e4m3x2_to_f16x2(h8);
-    const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&p16), *reinterpret_cast<const __half2*>(&back));
-    l8 = f16x2_to_e4m3x2(*reinterpret_cast<const uint32_t*>(&rest));
+// Four non-negative weights -> the codes of their high and low parts: 11 bits
+// to f16, 4 of them to e4m3, the exact rest to e4m3 again.
+__device__ __forceinline__ void split_weights(float a, float b, float c, float d, uint32_t& hi,
+                                              uint32_t& lo) {
+    const uint32_t p = pack_f16x2(a, b), q = pack_f16x2(c, d);
+    hi = f16x4_to_e4m3(p, q);
+    uint32_t x, y;
+    e4m3x4_to_f16(hi, x, y);
+    const __half2 r0 = __hsub2(*reinterpret_cast<const __half2*>(&p), *reinterpret_cast<const __half2*>(&x));
+    const __half2 r1 = __hsub2(*reinterpret_cast<const __half2*>(&q), *reinterpret_cast<const __half2*>(&y));
+    lo = f16x4_to_e4m3(*reinterpret_cast<const uint32_t*>(&r0), *reinterpret_cast<const uint32_t*>(&r1));
 }
 
 // One query row and head by one warp, fp32, reading only attended tokens
@@ -172,12 +179,10 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint32_t* bitmap = reinterpret_cast<uint32_t*>(smem + kOffUnion);  // [kMaxWords]
     uint32_t* wpre = bitmap + kMaxWords;                               // [kMaxWords]
-    int* ublk = reinterpret_cast<int*>(wpre + kMaxWords);              // [kMaxUnion] block
-    int* upage = ublk + kMaxUnion;                                     // page, or -1
-    uint32_t* umask = reinterpret_cast<uint32_t*>(upage + kMaxUnion);  // queries that selected it
-    float* uks = reinterpret_cast<float*>(umask + kMaxUnion);          // k scale
-    float* uve = uks + kMaxUnion;                                      // v scale = uvf * 2^uve
-    float* uvf = uve + kMaxUnion;
+    // per block of the union: first token (-1: bad page), queries that selected
+    // it, k scale, v scale; and its page
+    uint4* uinfo = reinterpret_cast<uint4*>(wpre + kMaxWords);         // [kMaxUnion]
+    int* upage = reinterpret_cast<int*>(uinfo + kMaxUnion);            // [kMaxUnion]
     Q8Window* wins = reinterpret_cast<Q8Window*>(smem + kOffWin);      // [kMaxQT]
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
     uint64_t* kfull = bars;                // [kStages]
@@ -238,9 +243,14 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         prefetch_tensormap(&tm_v);
     }
     // ---------------- the union of the tile's selected blocks ----------------
+    // A thread's first entry is looked up (id, page, scales) while the union is
+    // counted, so the chain of global loads runs beside the barriers.
     const int nent = QT * a.topk;
+    const int32_t* tile_ids = a.ids + ((size_t)b * a.S + s0) * a.topk;
+    const int n_real = min(QT, a.S - s0) * a.topk;  // entries of queries that exist
+    const int j_mine = tid < n_real ? __ldg(tile_ids + tid) : -1;
     for (int w = tid; w < nwords; w += kThreads) bitmap[w] = 0u;
-    for (int e = tid; e < min(nent, kMaxUnion); e += kThreads) umask[e] = 0u;
+    for (int e = tid; e < min(nent, kMaxUnion); e += kThreads) uinfo[e].y = 0u;
     if (tid < kMaxQT) {
         Q8Window w{0, -1, 0};
         if (tid < QT && s0 + tid < a.S) w = q8_window(a, b * a.S + s0 + tid, b, s0 + tid);
@@ -252,10 +262,8 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
     }
     __syncthreads();
     // block of entry e if its query can attend a token of it, else -1
-    auto entry = [&](int e, int& qi) -> int {
-        qi = e / a.topk;
-        if (s0 + qi >= a.S) return -1;
-        const int j = __ldg(a.ids + ((size_t)b * a.S + s0) * a.topk + e);
+    auto entry = [&](int e, int qi) -> int {
+        const int j = e == tid ? j_mine : __ldg(tile_ids + e);
         if (j < 0 || j >= a.nb_max) {
             if (j != -1) raise_status(kStatusBadBlockId);
             return -1;
@@ -263,10 +271,26 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         const int first = j * a.bs;
         return first <= wins[qi].hi && first + a.bs > wins[qi].lo ? j : -1;
     };
-    for (int e = tid; e < nent; e += kThreads) {
-        int qi;
-        const int j = entry(e, qi);
-        if (j >= 0) atomicOr(&bitmap[j >> 5], 1u << (j & 31));
+    auto lookup = [&](int j, int& page, float& ks, float& vs) {
+        page = __ldg(a.table + (size_t)b * a.nb_max + j);
+        if (page < 0 || page >= a.num_pages) {
+            raise_status(kStatusBadPage);
+            page = -1;
+            ks = vs = 0.f;
+        } else {
+            const size_t cell = (size_t)page * a.H_kv + g;
+            ks = __ldg(a.ks + cell);
+            vs = __ldg(a.vs + cell);
+        }
+    };
+    int page_mine = -1;
+    float ks_mine = 0.f, vs_mine = 0.f;
+    for (int e = tid; e < n_real; e += kThreads) {
+        const int j = entry(e, e / a.topk);
+        if (j >= 0) {
+            atomicOr(&bitmap[j >> 5], 1u << (j & 31));
+            if (e == tid) lookup(j, page_mine, ks_mine, vs_mine);
+        }
     }
     __syncthreads();
     if (warp == 0) {  // exclusive prefix of the words' population counts
@@ -293,33 +317,24 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         if (lane == 31) *s_nunion = incl;
     }
     __syncthreads();
-    for (int e = tid; e < nent; e += kThreads) {
-        int qi;
+    for (int e = tid; e < n_real; e += kThreads) {
+        const int qi = e / a.topk;
         const int j = entry(e, qi);
         if (j >= 0) {
             const int pos = (int)wpre[j >> 5] + __popc(bitmap[j >> 5] & ((1u << (j & 31)) - 1u));
-            ublk[pos] = j;
-            atomicOr(&umask[pos], 1u << qi);
+            int page = page_mine;
+            float ks = ks_mine, vs = vs_mine;
+            if (e != tid) lookup(j, page, ks, vs);
+            // every query that selected the block writes the same values
+            uinfo[pos].x = page >= 0 ? (uint32_t)(j * a.bs) : ~0u;
+            uinfo[pos].z = __float_as_uint(ks);
+            uinfo[pos].w = __float_as_uint(fmaxf(vs, kMinVScale));
+            upage[pos] = page;
+            atomicOr(&uinfo[pos].y, 1u << qi);
         }
     }
     __syncthreads();
     const int nunion = *s_nunion;
-    for (int u = tid; u < nunion; u += kThreads) {
-        int page = a.table[(size_t)b * a.nb_max + ublk[u]];
-        if (page < 0 || page >= a.num_pages) {
-            raise_status(kStatusBadPage);
-            page = -1;
-        }
-        upage[u] = page;
-        const size_t cell = page >= 0 ? (size_t)page * a.H_kv + g : 0;
-        uks[u] = page >= 0 ? a.ks[cell] : 0.f;
-        // f in (1/2, 1]: f * 2^e with the weight of the codes at most 2^(x + e - m)
-        const float vs = page >= 0 ? fmaxf(a.vs[cell], kMinVScale) : 1.f;
-        const uint32_t bits = __float_as_uint(vs);
-        const bool pow2 = (bits & 0x7fffffu) == 0u;
-        uve[u] = (float)((int)(bits >> 23) - (pow2 ? 127 : 126));
-        uvf[u] = pow2 ? 1.f : __uint_as_float((bits & 0x7fffffu) | 0x3f000000u);
-    }
     const int nunits = nunion * upb;
     const int npairs = (nunits + 1) / 2;
     const long long ctx = a.ctx_len[b];
@@ -379,57 +394,51 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         named_barrier_sync(kQBarrier, kQThreads);
         tc_fence_after();
         if (lane == 0) {
-            uint32_t any_pv = 0u;  // O holds something
-            auto pv = [&](int j) -> bool {
-                const int vs = j % kStages;
-                const uint32_t vb = smem_u32(smem + kOffV + vs * kStageBytes);
+            // operand descriptors of stage 0; a stage is 1024 units of 16 bytes on
+            const uint64_t kd0 = sw128_desc(smem_u32(smem + kOffK));
+            const uint64_t vd0 = sw128_desc_mn(smem_u32(smem + kOffV), kUnitBytes);
+            const uint32_t o_col = tmem_base + kColO, q_col = tmem_base + kColQ;
+            bool fine = true;
+            auto pv = [&](int j) {
+                const int vs = j & (kStages - 1);
+                fine = fine && mbar_wait(&vfull[vs], (j / kStages) & 1);
+#pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int u = 2 * j + c;
-                    if (!mbar_wait(&pfull[u & 3], (u >> 2) & 1) ||
-                        !mbar_wait(&vfull[vs], (j / kStages) & 1)) {
-                        *s_abort = 1;
-                        return false;
-                    }
+                    fine = fine && mbar_wait(&pfull[u & 3], (u >> 2) & 1);
+                    if (!fine) break;
                     tc_fence_after();
-                    if (u < nunits && upage[u / upb] >= 0) {
-                        const uint32_t p = tmem_base + kColS + (u & 3) * 64;
+                    const uint32_t p = tmem_base + kColS + (u & 3) * 64;
+                    const uint64_t vd = vd0 + (uint32_t)(vs * (kStageBytes >> 4) + c * (kUnitBytes >> 4));
 #pragma unroll
-                        for (int part = 0; part < 2; ++part)
+                    for (int part = 0; part < 2; ++part)
 #pragma unroll
-                            for (int kt = 0; kt < kUnit / 32; ++kt) {
-                                tc_mma_f8_tmem_a(tmem_base + kColO, p + part * 16 + kt * 8,
-                                                 sw128_desc_mn(vb + c * kUnitBytes + kt * 4096, kUnitBytes),
-                                                 kIdescPV, any_pv);
-                                any_pv = 1u;
-                            }
-                    }
+                        for (int kt = 0; kt < kUnit / 32; ++kt)
+                            tc_mma_f8_tmem_a(o_col, p + part * 16 + kt * 8, vd + kt * (4096 >> 4), kIdescPV,
+                                             (u | part | kt) != 0 ? 1u : 0u);
                     tc_commit(&obar[u & 3]);
                 }
-                tc_commit(&vempty[vs]);
-                return true;
+                if (fine) tc_commit(&vempty[vs]);
             };
-            bool fine = true;
             for (int i = 0; i < npairs && fine; ++i) {
-                const int ks = i % kStages;
-                if (*s_abort || !mbar_wait(&kfull[ks], (i / kStages) & 1)) {
-                    *s_abort = 1;
-                    fine = false;
-                    break;
-                }
+                const int ks = i & (kStages - 1);
+                fine = mbar_wait(&kfull[ks], (i / kStages) & 1) && !*s_abort;
+                if (!fine) break;
                 tc_fence_after();
-                const uint32_t kb = smem_u32(smem + kOffK + ks * kStageBytes);
+                const uint64_t kd = kd0 + (uint32_t)(ks * (kStageBytes >> 4));
                 const uint32_t d = tmem_base + kColS + (i & 1) * 128;
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int kk = 0; kk < kHD / 32; ++kk)
-                        tc_mma_f8_tmem_a(d, tmem_base + kColQ + part * 32 + kk * 8, sw128_desc(kb) + 2 * kk,
-                                         kIdescQK, (part | kk) != 0 ? 1u : 0u);
-                tc_commit(&kempty[ks]);
+                        tc_mma_f8_tmem_a(d, q_col + part * 32 + kk * 8, kd + 2 * kk, kIdescQK,
+                                         (part | kk) != 0 ? 1u : 0u);
                 tc_commit(&sfull[i & 1]);
-                if (i > 0) fine = pv(i - 1);
+                tc_commit(&kempty[ks]);
+                if (i > 0) pv(i - 1);
             }
             if (fine && npairs > 0) pv(npairs - 1);
+            if (!fine) *s_abort = 1;
             // nothing of this thread may still run on the tensor core when the
             // TMEM is released; the epilogue waits for it too
             tc_commit(drain);
@@ -510,21 +519,34 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         uint64_t* my_dec = decided + grp * 4 + quarter;
         uint64_t* their_dec = decided + (grp ^ 1) * 4 + quarter;
         bool stop = false;
+        // The unit's block entry is read one pair ahead; (n_blk, n_sub) walk the
+        // group's units without a division.
+        int n_blk = grp / upb, n_sub = grp % upb;
+        uint4 n_info = uinfo[min(n_blk, kMaxUnion - 1)];
         for (int i = 0; i < npairs; ++i) {
             const int u = 2 * i + grp;
-            // the unit: its block's entry, first token, and what the row sees of it
-            const int blk = u < nunits ? u / upb : 0;
-            const int page = u < nunits ? upage[blk] : -1;
-            const uint32_t mask = umask[blk];
-            const int t0 = ublk[blk] * a.bs + (u - blk * upb) * kUnit;
+            const uint4 info = n_info;
+            const int t0 = (int)info.x + n_sub * kUnit;                    // its first token
+            const bool there = u < nunits && info.x != ~0u;
+            n_sub += 2;
+            while (n_sub >= upb) {
+                n_sub -= upb;
+                ++n_blk;
+            }
+            n_info = uinfo[min(n_blk, kMaxUnion - 1)];
             int lo = 0, hi = -1;  // attended columns lo .. hi
-            if (page >= 0 && (mask & qbit) != 0u) {
+            if (there && (info.y & qbit) != 0u) {
                 lo = max(win.lo - t0, 0);
                 hi = min(win.hi - t0, kUnit - 1);
             }
             const bool mine = hi >= lo;
             const bool warp_any = __any_sync(0xffffffffu, mine);
-            const float ks = uks[blk], ve = uve[blk], vf = uvf[blk];
+            // v scale = f * 2^e, f in (1/2, 1]
+            const float ks = __uint_as_float(info.z);
+            const bool pow2 = (info.w & 0x7fffffu) == 0u;
+            const int ve_i = (int)(info.w >> 23) - (pow2 ? 127 : 126);
+            const float ve = (float)ve_i;
+            const float vf = pow2 ? 1.f : __uint_as_float((info.w & 0x7fffffu) | 0x3f000000u);
             const uint32_t scol = lane_addr + kColS + (u & 3) * 64;
             if (!mbar_wait(&sfull[i & 1], (i >> 1) & 1)) {
                 *s_abort = 1;
@@ -627,24 +649,22 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    uint32_t hi8[2], lo8[2];
+                    float2 p[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const float2 x = ffma2(make_float2(__uint_as_float(sv[4 * e + 2 * k]),
                                                            __uint_as_float(sv[4 * e + 2 * k + 1])), mul2, add2);
-                        float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                        sum[k] = fadd2(sum[k], p);
+                        p[k] = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                        sum[k] = fadd2(sum[k], p[k]);
                         if (vf != 1.f) {
-                            p.x *= vf;
-                            p.y *= vf;
+                            p[k].x *= vf;
+                            p[k].y *= vf;
                         }
-                        split_weights(p.x, p.y, hi8[k], lo8[k]);
                     }
-                    pk[e] = __byte_perm(hi8[0], hi8[1], 0x5410);
-                    pk[16 + e] = __byte_perm(lo8[0], lo8[1], 0x5410);
+                    split_weights(p[0].x, p[0].y, p[1].x, p[1].y, pk[e], pk[16 + e]);
                 }
                 const float2 t = fadd2(sum[0], sum[1]);
-                l = fmaf(t.x + t.y, exp2_int(-(int)ve), l);
+                l = fmaf(t.x + t.y, exp2_int(-ve_i), l);
             } else {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) pk[e] = 0u;
@@ -665,13 +685,13 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                 }
             }
             tmem_wait_st();
-            // V rows of tokens past the context must be zero before the MMA
-            // reads them (this thread: half of row r / 2 of the unit)
-            if (page >= 0 && t0 > ctx32 - kUnit) {
-                const int vs = i % kStages;
+            // V rows of tokens past the context and of absent units must be zero
+            // before the MMA reads them (this thread: half of row r / 2 of the unit)
+            if (!there || t0 > ctx32 - kUnit) {
+                const int vs = i & (kStages - 1);
                 if (!mbar_wait(&vfull[vs], (i / kStages) & 1)) *s_abort = 1;
                 const int vr = r >> 1;
-                if (t0 + vr >= ctx32) {
+                if (!there || t0 + vr >= ctx32) {
                     unsigned char* vt = smem + kOffV + vs * kStageBytes + grp * kUnitBytes + vr * 128;
 #pragma unroll
                     for (int c = 4 * (r & 1); c < 4 * (r & 1) + 4; ++c)

@@ -26,12 +26,21 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
     asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(r) : "r"(codes));
     return r;
 }
+// The four codes of a word -> two f16x2.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
 __device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
     return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 // Four codes of a word -> fp32.
 __device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float (&f)[4]) {
-    const float2 a = f16x2_to_f32(e4m3x2_to_f16x2(w)), b = f16x2_to_f32(e4m3x2_to_f16x2(w >> 16));
+    uint32_t lo, hi;
+    e4m3x4_to_f16(w, lo, hi);
+    const float2 a = f16x2_to_f32(lo), b = f16x2_to_f32(hi);
     f[0] = a.x;
     f[1] = a.y;
     f[2] = b.x;
@@ -48,7 +57,12 @@ __device__ __forceinline__ uint32_t f32_to_e4m3x2(float lo, float hi) {
     return r;
 }
 __device__ __forceinline__ uint32_t f32_to_e4m3x4(float a, float b, float c, float d) {
-    return f32_to_e4m3x2(a, b) | (f32_to_e4m3x2(c, d) << 16);
+    uint32_t r;
+    asm("{\n\t.reg .b16 x, y;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 y, %4, %3;\n\tmov.b32 %0, {x, y};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
 }
 
 // Smallest power of two 2^e, e >= kScaleMinExp, with amax <= 448 * 2^e
