@@ -19,11 +19,12 @@
 //   O += Phi V   + Plo V     M=128, N=128 dims, K=64 tokens, A = P from TMEM,
 //                            B = V MN-major from shared memory
 //
-// Scales. A block's k scale multiplies the fp32 logits. With the v scale
-// f * 2^e, f in (1/2, 1], the weight of the codes is 2^(x + e - m) * f and the
-// row sum adds 2^(x - m), so the running reference m of a row is the maximum of
-// x + e. Weights are 2^5 at the reference; it moves only when a unit passes it
-// by more than 3.75 (weights stay below 448), and O is rescaled only then.
+// Scales. A block's k scale multiplies the fp32 logits. Its v scale enters the
+// exponent, so that the weight is that of the codes, p = 2^(x + log2 vs - m),
+// and the row sum adds p / vs; the running reference m of a row is the maximum
+// of x + log2 vs. Weights are 2^5 at the reference; it moves only when a unit
+// passes it by more than 3.75 (weights stay below 448), and O is rescaled only
+// then.
 //
 // Warps: 0 TMA producer, 1 MMA issuer, 2..5 and 6..9 two softmax groups that
 // take the even and the odd units, one thread per row. A warp (two queries at
@@ -87,11 +88,6 @@ __device__ __forceinline__ void tc_mma_f8_tmem_a(uint32_t tmem_d, uint32_t tmem_
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
         "r"(tmem_a), "l"(b), "r"(idesc), "r"(accumulate));
-}
-
-// 2^e, e in -126 .. 127.
-__device__ __forceinline__ float exp2_int(int e) {
-    return __uint_as_float((uint32_t)(max(e, -126) + 127) << 23);
 }
 
 // Two f16x2 -> four e4m3 codes.
@@ -180,7 +176,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
     uint32_t* bitmap = reinterpret_cast<uint32_t*>(smem + kOffUnion);  // [kMaxWords]
     uint32_t* wpre = bitmap + kMaxWords;                               // [kMaxWords]
     // per block of the union: first token (-1: bad page), queries that selected
-    // it, k scale, v scale; and its page
+    // it, k scale, log2 of the v scale; and its page
     uint4* uinfo = reinterpret_cast<uint4*>(wpre + kMaxWords);         // [kMaxUnion]
     int* upage = reinterpret_cast<int*>(uinfo + kMaxUnion);            // [kMaxUnion]
     Q8Window* wins = reinterpret_cast<Q8Window*>(smem + kOffWin);      // [kMaxQT]
@@ -328,7 +324,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
             // every query that selected the block writes the same values
             uinfo[pos].x = page >= 0 ? (uint32_t)(j * a.bs) : ~0u;
             uinfo[pos].z = __float_as_uint(ks);
-            uinfo[pos].w = __float_as_uint(fmaxf(vs, kMinVScale));
+            uinfo[pos].w = __float_as_uint(log2f(fmaxf(vs, kMinVScale)));
             upage[pos] = page;
             atomicOr(&uinfo[pos].y, 1u << qi);
         }
@@ -461,13 +457,12 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         // ---- query row -> TMEM: group 0 stores the high parts, group 1 the low ----
         {
             const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + qrow * kHD);
-            uint4 w[16];
             float amax = 0.f;
             bool odd = false;  // not finite
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-                w[c] = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+                const uint4 w = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float2 f = bf16x2_to_f32(x[k]);
@@ -481,30 +476,36 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
             e = e < -100 ? -100 : e > 127 ? 127 : e;
             const float up = __uint_as_float((uint32_t)(7 - e + 127) << 23);  // largest element in [2^7, 2^8)
             unit *= __uint_as_float((uint32_t)(e - 7 + 127) << 23);
-            uint32_t part[32];
+            if (grp < 2) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t part[16];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float2 f0 = bf16x2_to_f32(x[2 * k]), f1 = bf16x2_to_f32(x[2 * k + 1]);
-                    f0.x *= up;
-                    f0.y *= up;
-                    f1.x *= up;
-                    f1.y *= up;
-                    const uint32_t h0 = f32_to_e4m3x2(f0.x, f0.y), h1 = f32_to_e4m3x2(f1.x, f1.y);
-                    uint32_t word = h0 | (h1 << 16);
-                    if (grp == 1) {
-                        const float2 b0 = f16x2_to_f32(e4m3x2_to_f16x2(h0)), b1 = f16x2_to_f32(e4m3x2_to_f16x2(h1));
-                        word = f32_to_e4m3x4(f0.x - b0.x, f0.y - b0.y, f1.x - b1.x, f1.y - b1.y);
+                    for (int c = 0; c < 8; ++c) {  // again, from L1: the row is not held
+                        const uint4 w = real ? __ldg(src + 8 * half + c) : make_uint4(0, 0, 0, 0);
+                        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float2 f0 = bf16x2_to_f32(x[2 * k]), f1 = bf16x2_to_f32(x[2 * k + 1]);
+                            f0.x *= up;
+                            f0.y *= up;
+                            f1.x *= up;
+                            f1.y *= up;
+                            uint32_t word = f32_to_e4m3x4(f0.x, f0.y, f1.x, f1.y);
+                            if (grp == 1) {
+                                float hi[4];
+                                e4m3x4_to_f32(word, hi);
+                                word = f32_to_e4m3x4(f0.x - hi[0], f0.y - hi[1], f1.x - hi[2], f1.y - hi[3]);
+                            }
+                            part[2 * c + k] = word;
+                        }
                     }
-                    part[2 * c + k] = word;
+                    tmem_st16(lane_addr + kColQ + grp * 32 + half * 16, part);
                 }
+                tmem_wait_st();
+                tc_fence_before();
+                named_barrier_sync(kQBarrier, kQThreads);
             }
-            tmem_st32(lane_addr + kColQ + grp * 32, part);
-            tmem_wait_st();
-            tc_fence_before();
-            named_barrier_sync(kQBarrier, kQThreads);
         }
         float slope2 = 0.f, cap2 = 0.f, inv_cap = 0.f;
         if constexpr (MODS) {
@@ -541,12 +542,8 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
             }
             const bool mine = hi >= lo;
             const bool warp_any = __any_sync(0xffffffffu, mine);
-            // v scale = f * 2^e, f in (1/2, 1]
             const float ks = __uint_as_float(info.z);
-            const bool pow2 = (info.w & 0x7fffffu) == 0u;
-            const int ve_i = (int)(info.w >> 23) - (pow2 ? 127 : 126);
-            const float ve = (float)ve_i;
-            const float vf = pow2 ? 1.f : __uint_as_float((info.w & 0x7fffffu) | 0x3f000000u);
+            const float lv = __uint_as_float(info.w);  // log2 of the v scale
             const uint32_t scol = lane_addr + kColS + (u & 3) * 64;
             if (!mbar_wait(&sfull[i & 1], (i >> 1) & 1)) {
                 *s_abort = 1;
@@ -605,7 +602,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                     for (int e = 0; e < 64; ++e) sv[e] = __float_as_uint(xs[e]);
                     mul = 1.f;
                 }
-                if (hi - lo != kUnit - 1) {
+                if (__any_sync(0xffffffffu, mine && hi - lo != kUnit - 1)) {
 #pragma unroll
                     for (int e = 0; e < 64; ++e)
                         sv[e] = e >= lo && e <= hi ? sv[e] : __float_as_uint(-INFINITY);
@@ -617,7 +614,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                 for (int e = 8; e < 64; e += 2)
                     pm[(e >> 1) & 7] = fmax3(pm[(e >> 1) & 7], __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
                 mx = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
-                mx = mx * mul + ve;
+                mx = mine ? mx * mul + lv : -INFINITY;
             }
             // the reference after the unit before this one, then after this one
             if (grp == 1 || i > 0) {
@@ -644,7 +641,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
             if (lane == 0) mbar_arrive(my_dec);
             uint32_t pk[32];  // 16 words of high parts, 16 of low parts
             if (mine) {
-                const float add = ve + kShift - m;
+                const float add = lv + kShift - m;
                 const float2 mul2 = make_float2(mul, mul), add2 = make_float2(add, add);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -656,15 +653,11 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                                                            __uint_as_float(sv[4 * e + 2 * k + 1])), mul2, add2);
                         p[k] = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                         sum[k] = fadd2(sum[k], p[k]);
-                        if (vf != 1.f) {
-                            p[k].x *= vf;
-                            p[k].y *= vf;
-                        }
                     }
                     split_weights(p[0].x, p[0].y, p[1].x, p[1].y, pk[e], pk[16 + e]);
                 }
                 const float2 t = fadd2(sum[0], sum[1]);
-                l = fmaf(t.x + t.y, exp2_int(-ve_i), l);
+                l = fmaf(t.x + t.y, fast_exp2(-lv), l);
             } else {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) pk[e] = 0u;
