@@ -104,9 +104,10 @@ __device__ __forceinline__ float q8_score(float z, float cap, float inv_cap, flo
 constexpr int kQ8SimtWarps = 4;
 constexpr int kQ8MaxHd = 256;
 
-template <typename T>
+// HD: the largest head_dim of the instance (64, 128 or 256).
+template <typename T, int HD>
 __global__ void __launch_bounds__(kQ8SimtWarps * 32) sparse_attn_q8_simt_kernel(const AttnQ8Args a) {
-    constexpr int kPer = kQ8MaxHd / 32;
+    constexpr int kPer = HD / 32;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     float* sq = reinterpret_cast<float*>(smem_raw);                                // [hd] query, fp32
     float* so = sq + a.hd;                         // [warps][hd]
@@ -153,6 +154,7 @@ __global__ void __launch_bounds__(kQ8SimtWarps * 32) sparse_attn_q8_simt_kernel(
                     if (see) {
                         const uint4* kr = reinterpret_cast<const uint4*>(kb + (size_t)u * hd);
                         float dot = 0.f;
+#pragma unroll 4
                         for (int c = 0; c < hd / 16; ++c) {
                             const uint4 w4 = __ldg(kr + c);
                             const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
@@ -183,14 +185,24 @@ __global__ void __launch_bounds__(kQ8SimtWarps * 32) sparse_attn_q8_simt_kernel(
                     blk_m = m_new;
 #pragma unroll
                     for (int e = 0; e < kPer; ++e) o[e] *= corr;
-                    // only tokens in the window are read: others may be unset memory
-                    for (uint32_t left = seen; left != 0u; left &= left - 1u) {
-                        const int t1 = __ffs(left) - 1;
-                        const float p1 = __shfl_sync(0xffffffffu, pw, t1) * vmul;
+                    // only tokens in the window are read: others may be unset memory;
+                    // eight tokens' codes are in flight at a time
+                    for (int t1 = 0; t1 < 32; t1 += 8) {
+                        if (((seen >> t1) & 0xffu) == 0u) continue;
                         const uint8_t* vr = vb + (size_t)(u0 + t1) * hd + lane;
+                        uint8_t c[8][kPer];
 #pragma unroll
-                        for (int e = 0; e < kPer; ++e)
-                            if (e < per_lane) o[e] = fmaf(p1, e4m3_to_f32(__ldg(vr + 32 * e)), o[e]);
+                        for (int k = 0; k < 8; ++k)
+#pragma unroll
+                            for (int e = 0; e < kPer; ++e)
+                                c[k][e] = e < per_lane && ((seen >> (t1 + k)) & 1u) ? __ldg(vr + (size_t)k * hd + 32 * e) : 0;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float p1 = __shfl_sync(0xffffffffu, pw, t1 + k) * vmul;
+#pragma unroll
+                            for (int e = 0; e < kPer; ++e)
+                                if (e < per_lane && ((seen >> (t1 + k)) & 1u)) o[e] = fmaf(p1, e4m3_to_f32(c[k][e]), o[e]);
+                        }
                     }
                 }
             }

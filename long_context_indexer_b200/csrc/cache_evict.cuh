@@ -13,7 +13,7 @@ namespace bwu {
 constexpr int kRange = 1024;   // blocks of a sequence one cluster accumulates
 constexpr int kMaxSplit = 16;  // CTAs of a cluster, each taking a share of the rows
 constexpr int kMaxWarps = 32;
-constexpr int kRowsAhead = 8;  // rows a warp loads before it adds them
+constexpr int kRowsAhead = 16;  // rows a warp loads before it adds them (one where it has one)
 constexpr size_t smem_bytes(int warps) { return (size_t)warps * kRange * 4 + kRange * 8; }
 }  // namespace bwu
 
@@ -27,6 +27,7 @@ constexpr size_t smem_bytes(int warps) { return (size_t)warps * kRange * 4 + kRa
 // the cluster adds the CTAs' (distributed shared memory) to the weight. A
 // sequence of more than kRange blocks is cut into ranges, each with its own
 // cluster that reads every entry and keeps those of its range.
+template <int kAhead>
 __global__ void __launch_bounds__(bwu::kMaxWarps * 32) block_weight_update_kernel(
     const int32_t* __restrict__ ids, const float* __restrict__ mass, int S, int H_kv, int topk,
     int nb_max, float decay, float* __restrict__ weight, int nsplit) {
@@ -45,27 +46,27 @@ __global__ void __launch_bounds__(bwu::kMaxWarps * 32) block_weight_update_kerne
     __syncwarp();
     const int stride = nsplit * nw;
     const size_t step = (size_t)stride * topk;  // entries between two rows of this warp
-    for (int s0 = split * nw + warp; s0 < S; s0 += stride * kRowsAhead) {
+    for (int s0 = split * nw + warp; s0 < S; s0 += stride * kAhead) {
         for (int i = lane; i < ((topk + 31) & ~31); i += 32) {
             const size_t at = ((size_t)b * S + s0) * topk + i;
             const int32_t* idp = ids + at;
             const float* mp = mass + (((size_t)b * S + s0) * H_kv * topk + i);
-            const int rows = i < topk ? min(kRowsAhead, (S - s0 + stride - 1) / stride) : 0;
-            int id[kRowsAhead];
-            float add[kRowsAhead];
+            const int rows = i < topk ? min(kAhead, (S - s0 + stride - 1) / stride) : 0;
+            int id[kAhead];
+            float add[kAhead];
 #pragma unroll
-            for (int k = 0; k < kRowsAhead; ++k) {
+            for (int k = 0; k < kAhead; ++k) {
                 id[k] = k < rows ? __ldg(idp + k * step) : -1;
                 add[k] = k < rows ? __ldg(mp + k * step * H_kv) : 0.f;
             }
             for (int g = 1; g < H_kv; ++g) {
                 mp += topk;
 #pragma unroll
-                for (int k = 0; k < kRowsAhead; ++k)
+                for (int k = 0; k < kAhead; ++k)
                     add[k] += k < rows ? __ldg(mp + k * step * H_kv) : 0.f;
             }
 #pragma unroll
-            for (int k = 0; k < kRowsAhead; ++k) {
+            for (int k = 0; k < kAhead; ++k) {
                 const unsigned at_j = (unsigned)(id[k] - j0);
                 if (at_j < (unsigned)width)
                     mine[at_j] += add[k];
@@ -163,6 +164,11 @@ __global__ void __launch_bounds__(1024) cache_evict_kernel(
     const int32_t* trow = table + (size_t)b * nb_max;
     const float* wrow = weight + (size_t)b * nb_max;
     const int jt = split * IPT * nt + tid;  // this thread's first block
+    for (int e = tid; e < kBins; e += nt) s_own[e] = 0;
+    if (nsplit > 1) {
+        for (int e = tid; e < 3 * kBins; e += nt) s_sum[0][e] = 0;
+        cluster_arrive();  // waited for before the first remote addition
+    }
     int page[IPT];
     float w[IPT];
 #pragma unroll
@@ -216,6 +222,7 @@ __global__ void __launch_bounds__(1024) cache_evict_kernel(
                 cand |= 1u << i;
         }
     }
+    if (nsplit > 1) cluster_wait();
     const int m = budget - sink - recent;  // candidates to keep, fewer than there are
     if (trim && m > 0) {                   // the same for every thread of the cluster
         uint32_t key[IPT];
@@ -224,10 +231,7 @@ __global__ void __launch_bounds__(1024) cache_evict_kernel(
         uint32_t t = 0u, known = 0u;  // digits found so far, and their bits
         int need = m;                 // entries still to take among those that match t
         bool whole = false;           // all that match t are taken
-        for (int e = tid; e < kBins; e += nt) s_own[e] = 0;
-        if (nsplit > 1)
-            for (int e = tid; e < 3 * kBins; e += nt) s_sum[0][e] = 0;
-        cluster_sync();
+        __syncthreads();
 #pragma unroll 1
         for (int pass = 0; pass < 3 && !whole; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;

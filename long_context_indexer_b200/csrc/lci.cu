@@ -1461,8 +1461,10 @@ lci_status launch_attn_q8_simt(const lci::AttnQ8Args& a, int32_t batch, cudaStre
     const size_t smem = (size_t)(a.hd * (1 + lci::kQ8SimtWarps) + 2 * lci::kQ8SimtWarps +
                                  3 * a.topk) * 4;
     const dim3 grid((unsigned)(batch * a.S), (unsigned)a.H_kv);
-    const cudaError_t e = launch_early(lci::sparse_attn_q8_simt_kernel<T>, grid,
-                                       dim3(lci::kQ8SimtWarps * 32), smem, st, 1, a);
+    auto kern = a.hd <= 64 ? lci::sparse_attn_q8_simt_kernel<T, 64>
+                           : a.hd <= 128 ? lci::sparse_attn_q8_simt_kernel<T, 128>
+                                         : lci::sparse_attn_q8_simt_kernel<T, 256>;
+    const cudaError_t e = launch_early(kern, grid, dim3(lci::kQ8SimtWarps * 32), smem, st, 1, a);
     if (e != cudaSuccess) return fail(LCI_ERR_CUDA, "sparse_attn_q8: %s", cudaGetErrorString(e));
     return check_launch("sparse_attn_q8");
 }
@@ -1780,9 +1782,12 @@ lci_status lci_block_weight_update(const int32_t* d_ids, const float* d_mass, in
     if (topk > lci::kMaxTopk || max_blocks > kMaxNbMax || batch > 65535)
         return fail(LCI_ERR_UNSUPPORTED, "block_weight_update: topk above %d, max_blocks above %d or "
                     "batch above 65535", lci::kMaxTopk, kMaxNbMax);
-    static KernelSetup setup;
-    const cudaError_t se = setup.prepare(lci::block_weight_update_kernel,
-                                         (int)lci::bwu::smem_bytes(lci::bwu::kMaxWarps), true);
+    static KernelSetup setup_one, setup_many;
+    auto one = lci::block_weight_update_kernel<1>;
+    auto many = lci::block_weight_update_kernel<lci::bwu::kRowsAhead>;
+    const bool few = S <= 4;  // a row per warp
+    const cudaError_t se = (few ? setup_one : setup_many).prepare(few ? one : many,
+            (int)lci::bwu::smem_bytes(lci::bwu::kMaxWarps), true);
     if (se != cudaSuccess)
         return fail(LCI_ERR_CUDA, "block_weight_update: %s", cudaGetErrorString(se));
     // Rows are spread over warps, then over the CTAs of a cluster (while the
@@ -1795,7 +1800,7 @@ lci_status lci_block_weight_update(const int32_t* d_ids, const float* d_mass, in
            2ll * nsplit * ranges * batch <= 148)
         nsplit *= 2;
     const cudaError_t e = launch_early(
-        lci::block_weight_update_kernel, dim3((unsigned)nsplit, (unsigned)ranges, (unsigned)batch),
+        few ? one : many, dim3((unsigned)nsplit, (unsigned)ranges, (unsigned)batch),
         dim3((unsigned)warps * 32), lci::bwu::smem_bytes(warps), static_cast<cudaStream_t>(stream),
         nsplit, d_ids, d_mass, S, num_kv_heads, topk, max_blocks, decay, d_weight, nsplit);
     if (e != cudaSuccess) return fail(LCI_ERR_CUDA, "block_weight_update: %s", cudaGetErrorString(e));
