@@ -43,6 +43,7 @@ constexpr int kStrip = 16;
 constexpr int kRows = 16;       // query heads per MMA (padded)
 constexpr int kMaxSplit = 8;
 constexpr float kLazy = 8.f;
+constexpr int kPrefetch = 16;   // strips (64 KiB) a warp may ask for ahead
 // shared memory, in floats. O rows: four segments of HD/4 dims, each padded by 8
 // and the row by 4, so that 8 lanes' 16-byte stores meet 32 different banks.
 template <int HD> __host__ __device__ constexpr int seg_pitch() { return HD / 4 + 8; }
@@ -216,9 +217,11 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
     unsigned long long cell_lane = 0;
     float ks_lane = 0.f, vs_lane = 0.f;
     uint32_t live = 0u;
-    int n_blk = -1, st = 0, st_end = 0, n_t0 = 0;
-    float n_ks = 0.f, n_vs = 0.f;
+    int n_blk = -1, n_x = 0, st = 0, st_end = 0, n_t0 = 0;
     const uint8_t *kp = nullptr, *vp = nullptr;
+    // A warp with few strips asks L2 for all of them at once: one round trip to
+    // HBM (and to the page tables of a large pool) instead of one per strip.
+    const bool few = w1 - w0 <= kPrefetch;
     auto lookup = [&](int j) {
         t_lane = -1;
         const int page = q8_page(a, b, j, win);
@@ -227,6 +230,13 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
             cell_lane = (unsigned long long)page * a.H_kv + g;
             ks_lane = a.ks[cell_lane];
             vs_lane = a.vs[cell_lane];
+            if (few) {
+                const int f = (base + lane) * spb;
+                const int s0 = max(w0 - f, 0), s1 = min(w1 - f, spb);
+                const size_t at = (cell_lane * a.bs + s0 * kStrip) * HD;
+                prefetch_l2_bulk(a.k + at, (uint32_t)(s1 - s0) * kStrip * HD);
+                prefetch_l2_bulk(a.v + at, (uint32_t)(s1 - s0) * kStrip * HD);
+            }
         }
         live = __ballot_sync(0xffffffffu, t_lane >= 0);
     };
@@ -237,9 +247,8 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
                 const int x = __ffs(live) - 1;
                 live &= live - 1u;
                 n_blk = base + x;
+                n_x = x;
                 n_t0 = __shfl_sync(0xffffffffu, t_lane, x);
-                n_ks = __shfl_sync(0xffffffffu, ks_lane, x);
-                n_vs = __shfl_sync(0xffffffffu, vs_lane, x);
                 const unsigned long long c = __shfl_sync(0xffffffffu, cell_lane, x);
                 kp = a.k + c * a.bs * HD;
                 vp = a.v + c * a.bs * HD;
@@ -328,8 +337,9 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
 
     while (have) {
         const int c_blk = n_blk, c_t0 = n_t0 + st * kStrip;
-        const float c_ks = n_ks;
-        const VScale c_vs = split_v_scale(n_vs);
+        // a block's scales stay with the lane that looked it up until now
+        const float c_ks = __shfl_sync(0xffffffffu, ks_lane, n_x);
+        const VScale c_vs = split_v_scale(__shfl_sync(0xffffffffu, vs_lane, n_x));
         const bool more = advance();
         if (more) nxt.load(kp + (size_t)st * kStrip * HD, vp + (size_t)st * kStrip * HD, g8, q4);
 
@@ -362,14 +372,40 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float z = sc[j][e] * (e < 2 ? ca : cb);
-                if constexpr (MODS)
-                    x[j][e] = q8_score(z, a.cap, inv_cap, e < 2 ? slope_a : slope_b,
-                                       abs(win.p - (ta + 8 * j + (e & 1)))) + c_vs.e;
-                else
-                    x[j][e] = z + c_vs.e;
+            for (int e = 0; e < 4; ++e) x[j][e] = sc[j][e] * (e < 2 ? ca : cb);
+        if constexpr (MODS) {
+            if (a.cap > 0.f) {
+                float big = 0.f;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[j][e] *= inv_cap;
+                        big = fmaxf(big, fabsf(x[j][e]));
+                    }
+                // one branch for the warp: mostly every |u| is small
+                if (__any_sync(0xffffffffu, !(big <= kTanhSmall))) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[j][e] = a.cap * q8_tanh(x[j][e]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[j][e] = a.cap * q8_tanh_small(x[j][e]);
+                }
             }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[j][e] = fmaf(-(e < 2 ? slope_a : slope_b), (float)abs(win.p - (ta + 8 * j + (e & 1))), x[j][e]) * kLog2e;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[j][e] += c_vs.e;
         const bool partial = c_t0 < win.lo || c_t0 + kStrip - 1 > win.hi;
         if (partial) {
 #pragma unroll

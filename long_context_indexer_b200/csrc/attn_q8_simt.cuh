@@ -84,14 +84,15 @@ constexpr float kTanhSmall = 0.625f;
 constexpr float kTanhC0 = -0.3333328068256378f, kTanhC1 = 0.13331441581249237f,
                 kTanhC2 = -0.05373971164226532f, kTanhC3 = 0.020639076828956604f,
                 kTanhC4 = -0.00570497615262866f;
+__device__ __forceinline__ float q8_tanh_small(float u) {
+    const float v = u * u;
+    const float p = fmaf(v, fmaf(v, fmaf(v, fmaf(v, kTanhC4, kTanhC3), kTanhC2), kTanhC1), kTanhC0);
+    return fmaf(u * v, p, u);
+}
 __device__ __forceinline__ float q8_tanh(float u) {
     const float a = fabsf(u);
-    if (a <= kTanhSmall) {
-        const float v = u * u;
-        const float p = fmaf(v, fmaf(v, fmaf(v, fmaf(v, kTanhC4, kTanhC3), kTanhC2), kTanhC1), kTanhC0);
-        return fmaf(u * v, p, u);
-    }
-    return copysignf(1.f - __fdividef(2.f, fast_exp2(2.f * kLog2e * a) + 1.f), u);  // NaN stays NaN
+    const float far = copysignf(1.f - __fdividef(2.f, fast_exp2(2.f * kLog2e * a) + 1.f), u);
+    return a <= kTanhSmall ? q8_tanh_small(u) : far;  // NaN stays NaN
 }
 
 // A scaled logit in natural units -> capped and biased, in log2 units.
