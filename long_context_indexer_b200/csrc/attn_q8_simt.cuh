@@ -84,6 +84,10 @@ constexpr float kTanhSmall = 0.625f;
 constexpr float kTanhC0 = -0.3333328068256378f, kTanhC1 = 0.13331441581249237f,
                 kTanhC2 = -0.05373971164226532f, kTanhC3 = 0.020639076828956604f,
                 kTanhC4 = -0.00570497615262866f;
+// the same with three coefficients for |u| <= 0.25 (relative error 3e-9)
+constexpr float kTanhTiny = 0.25f;
+constexpr float kTanhT0 = -0.3333323895931244f, kTanhT1 = 0.13324236869812012f,
+                kTanhT2 = -0.05143002048134804f;
 __device__ __forceinline__ float q8_tanh_small(float u) {
     const float v = u * u;
     const float p = fmaf(v, fmaf(v, fmaf(v, fmaf(v, kTanhC4, kTanhC3), kTanhC2), kTanhC1), kTanhC0);

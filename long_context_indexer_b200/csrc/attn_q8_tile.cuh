@@ -15,9 +15,10 @@
 // largest weight). Both products take two MMAs at twice the bf16 rate: the same
 // tensor time as a bf16 cache, half its shared-memory traffic, and no
 // conversion of 64 KiB per pair.
-//   S  = Qhi K^T + Qlo K^T   M=128, N=128 tokens, A = Q from TMEM
+//   S  = Qhi K^T + Qlo K^T   M=128, N=128 tokens, A = Q from shared memory
 //   O += Phi V   + Plo V     M=128, N=128 dims, K=64 tokens, A = P from TMEM,
 //                            B = V MN-major from shared memory
+// (Q stays out of TMEM so that three pairs of S fit beside O.)
 //
 // Scales. A block's k scale multiplies the fp32 logits. Its v scale enters the
 // exponent, so that the weight is that of the codes, p = 2^(x + log2 vs - m),
@@ -62,15 +63,17 @@ constexpr int kMaxWords = 512;         // block bitmap words: nb_max <= 16384
 constexpr int kMaxUnion = 2048;        // distinct blocks per tile
 constexpr int kGroupWarps = 4;
 constexpr int kThreads = 64 + 2 * 32 * kGroupWarps;
-// TMEM columns: O fp32, two pairs of S (fp32; a unit's 64 columns then hold its
-// P as 16 columns of high and 16 of low parts), Q high and low parts
-constexpr int kColO = 0, kColS = 128, kColQ = 384, kTmemCols = 512;
+constexpr int kSlots = 3;              // pairs of S in flight
+// TMEM columns: O fp32, kSlots pairs of S (fp32; a unit's 64 columns then hold
+// its P as 16 columns of high and 16 of low parts)
+constexpr int kColO = 0, kColS = 128, kTmemCols = 512;
 constexpr float kShift = 5.f;          // log2 of the weight at the reference
 constexpr float kLazy = 3.75f;         // 2^(5 + 3.75) < 448
 // shared memory (offsets from a 1024-byte aligned base)
 constexpr int kOffK = 0;
 constexpr int kOffV = kOffK + kStages * kStageBytes;
-constexpr int kOffUnion = kOffV + kStages * kStageBytes;
+constexpr int kOffQ = kOffV + kStages * kStageBytes;     // high parts, then low parts
+constexpr int kOffUnion = kOffQ + 2 * kRows * kHD;
 constexpr int kUnionBytes = 2 * kMaxWords * 4 + kMaxUnion * (16 + 4);
 constexpr int kOffWin = kOffUnion + kUnionBytes;    // [kMaxQT] Q8Window
 constexpr int kOffBar = kOffWin + kMaxQT * 16;
@@ -88,6 +91,15 @@ __device__ __forceinline__ void tc_mma_f8_tmem_a(uint32_t tmem_d, uint32_t tmem_
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
         "r"(tmem_a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+
+// D (+)= A B, 8-bit operands in shared memory.
+__device__ __forceinline__ void tc_mma_f8(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
 }
 
 // Two f16x2 -> four e4m3 codes.
@@ -185,16 +197,16 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
     uint64_t* kempty = kfull + kStages;    // [kStages]
     uint64_t* vfull = kempty + kStages;    // [kStages]
     uint64_t* vempty = vfull + kStages;    // [kStages]
-    uint64_t* sfull = vempty + kStages;    // [2] a pair's S written
-    uint64_t* pfull = sfull + 2;           // [4] a unit's P written (4 warps)
-    uint64_t* decided = pfull + 4;         // [2][4] a group's reference of a unit, per 32 rows
-    uint64_t* obar = decided + 8;          // [4] a unit's P V completed
-    uint64_t* drain = obar + 4;            // every MMA of the tile completed
+    uint64_t* sfull = vempty + kStages;      // [kSlots] a pair's S written
+    uint64_t* pfull = sfull + kSlots;        // [2 * kSlots] a unit's P written (4 warps)
+    uint64_t* decided = pfull + 2 * kSlots;  // [2][4] a group's reference of a unit, per 32 rows
+    uint64_t* obar = decided + 8;            // [2 * kSlots] a unit's P V completed
+    uint64_t* drain = obar + 2 * kSlots;     // every MMA of the tile completed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     int* s_nunion = reinterpret_cast<int*>(tmem_slot + 1);
     // set by any role whose bounded wait ran out: every role then stops
     volatile int* s_abort = s_nunion + 1;
-    static_assert((4 * kStages + 2 + 4 + 8 + 4 + 1) * 8 + 12 <= 512, "barriers fit");
+    static_assert((4 * kStages + 5 * kSlots + 8 + 1) * 8 + 12 <= 512, "barriers fit");
     float* mref = reinterpret_cast<float*>(smem + kOffRow);  // [128]
     float* lsum = mref + 128;                                // [2][128]
     int* redo = reinterpret_cast<int*>(lsum + 256);          // [128]
@@ -219,10 +231,12 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
             mbar_init(&vfull[i], 1);
             mbar_init(&vempty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) mbar_init(&sfull[i], 1);
-        for (int i = 0; i < 4; ++i) mbar_init(&pfull[i], kGroupWarps);
+        for (int i = 0; i < kSlots; ++i) mbar_init(&sfull[i], 1);
+        for (int i = 0; i < 2 * kSlots; ++i) {
+            mbar_init(&pfull[i], kGroupWarps);
+            mbar_init(&obar[i], 1);
+        }
         for (int i = 0; i < 8; ++i) mbar_init(&decided[i], 1);
-        for (int i = 0; i < 4; ++i) mbar_init(&obar[i], 1);
         mbar_init(drain, 1);
         *s_abort = 0;
         fence_mbar_init();
@@ -339,7 +353,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    // named barrier 1: the MMA warp waits for the query rows in TMEM;
+    // named barrier 1: the MMA warp waits for the query rows in shared memory;
     // named barrier 2: the softmax warps before the epilogue
     constexpr int kQBarrier = 1, kQThreads = 32 + 64 * kGroupWarps;
     constexpr int kEndBarrier = 2, kEndThreads = 64 * kGroupWarps;
@@ -393,26 +407,26 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
             // operand descriptors of stage 0; a stage is 1024 units of 16 bytes on
             const uint64_t kd0 = sw128_desc(smem_u32(smem + kOffK));
             const uint64_t vd0 = sw128_desc_mn(smem_u32(smem + kOffV), kUnitBytes);
-            const uint32_t o_col = tmem_base + kColO, q_col = tmem_base + kColQ;
+            const uint64_t qd0 = sw128_desc(smem_u32(smem + kOffQ));
+            const uint32_t o_col = tmem_base + kColO;
             bool fine = true;
             auto pv = [&](int j) {
-                const int vs = j & (kStages - 1);
+                const int vs = j & (kStages - 1), slot = j % kSlots;
                 fine = fine && mbar_wait(&vfull[vs], (j / kStages) & 1);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int u = 2 * j + c;
-                    fine = fine && mbar_wait(&pfull[u & 3], (u >> 2) & 1);
+                    fine = fine && mbar_wait(&pfull[2 * slot + c], (j / kSlots) & 1);
                     if (!fine) break;
                     tc_fence_after();
-                    const uint32_t p = tmem_base + kColS + (u & 3) * 64;
+                    const uint32_t p = tmem_base + kColS + slot * 128 + c * 64;
                     const uint64_t vd = vd0 + (uint32_t)(vs * (kStageBytes >> 4) + c * (kUnitBytes >> 4));
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int kt = 0; kt < kUnit / 32; ++kt)
                             tc_mma_f8_tmem_a(o_col, p + part * 16 + kt * 8, vd + kt * (4096 >> 4), kIdescPV,
-                                             (u | part | kt) != 0 ? 1u : 0u);
-                    tc_commit(&obar[u & 3]);
+                                             (j | c | part | kt) != 0 ? 1u : 0u);
+                    tc_commit(&obar[2 * slot + c]);
                 }
                 if (fine) tc_commit(&vempty[vs]);
             };
@@ -422,18 +436,19 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                 if (!fine) break;
                 tc_fence_after();
                 const uint64_t kd = kd0 + (uint32_t)(ks * (kStageBytes >> 4));
-                const uint32_t d = tmem_base + kColS + (i & 1) * 128;
+                // the slot's last pair, i - kSlots, has had its P V issued
+                const uint32_t d = tmem_base + kColS + (i % kSlots) * 128;
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int kk = 0; kk < kHD / 32; ++kk)
-                        tc_mma_f8_tmem_a(d, q_col + part * 32 + kk * 8, kd + 2 * kk, kIdescQK,
-                                         (part | kk) != 0 ? 1u : 0u);
-                tc_commit(&sfull[i & 1]);
+                        tc_mma_f8(d, qd0 + part * (kRows * kHD >> 4) + 2 * kk, kd + 2 * kk, kIdescQK,
+                                  (part | kk) != 0 ? 1u : 0u);
+                tc_commit(&sfull[i % kSlots]);
                 tc_commit(&kempty[ks]);
-                if (i > 0) pv(i - 1);
+                if (i >= kSlots - 1) pv(i - (kSlots - 1));
             }
-            if (fine && npairs > 0) pv(npairs - 1);
+            for (int j = max(0, npairs - (kSlots - 1)); j < npairs && fine; ++j) pv(j);
             if (!fine) *s_abort = 1;
             // nothing of this thread may still run on the tensor core when the
             // TMEM is released; the epilogue waits for it too
@@ -454,7 +469,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         const uint32_t lane_addr = tmem_base + ((uint32_t)(quarter * 32) << 16);
         const int ctx32 = (int)(ctx < 0x7fffffffLL ? ctx : 0x7fffffffLL);
         float unit = MODS ? a.scale : a.scale * kLog2e;  // what raw S is multiplied by, with the k scale
-        // ---- query row -> TMEM: group 0 stores the high parts, group 1 the low ----
+        // ---- query row -> shared memory: group 0 stores the high parts, group 1 the low ----
         {
             const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + qrow * kHD);
             float amax = 0.f;
@@ -476,36 +491,34 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
             e = e < -100 ? -100 : e > 127 ? 127 : e;
             const float up = __uint_as_float((uint32_t)(7 - e + 127) << 23);  // largest element in [2^7, 2^8)
             unit *= __uint_as_float((uint32_t)(e - 7 + 127) << 23);
-            if (grp < 2) {
+            unsigned char* qt_row = smem + kOffQ + grp * (kRows * kHD) + r * kHD;
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t part[16];
+            for (int c = 0; c < 8; ++c) {  // 16 dims; again from L1: the row is not held
+                uint32_t word[4];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {  // again, from L1: the row is not held
-                        const uint4 w = real ? __ldg(src + 8 * half + c) : make_uint4(0, 0, 0, 0);
-                        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                for (int k = 0; k < 2; ++k) {
+                    const uint4 w = real ? __ldg(src + 2 * c + k) : make_uint4(0, 0, 0, 0);
+                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            float2 f0 = bf16x2_to_f32(x[2 * k]), f1 = bf16x2_to_f32(x[2 * k + 1]);
-                            f0.x *= up;
-                            f0.y *= up;
-                            f1.x *= up;
-                            f1.y *= up;
-                            uint32_t word = f32_to_e4m3x4(f0.x, f0.y, f1.x, f1.y);
-                            if (grp == 1) {
-                                float hi[4];
-                                e4m3x4_to_f32(word, hi);
-                                word = f32_to_e4m3x4(f0.x - hi[0], f0.y - hi[1], f1.x - hi[2], f1.y - hi[3]);
-                            }
-                            part[2 * c + k] = word;
+                    for (int n = 0; n < 2; ++n) {
+                        float2 f0 = bf16x2_to_f32(x[2 * n]), f1 = bf16x2_to_f32(x[2 * n + 1]);
+                        f0.x *= up;
+                        f0.y *= up;
+                        f1.x *= up;
+                        f1.y *= up;
+                        uint32_t codes = f32_to_e4m3x4(f0.x, f0.y, f1.x, f1.y);
+                        if (grp == 1) {
+                            float hi[4];
+                            e4m3x4_to_f32(codes, hi);
+                            codes = f32_to_e4m3x4(f0.x - hi[0], f0.y - hi[1], f1.x - hi[2], f1.y - hi[3]);
                         }
+                        word[2 * k + n] = codes;
                     }
-                    tmem_st16(lane_addr + kColQ + grp * 32 + half * 16, part);
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                named_barrier_sync(kQBarrier, kQThreads);
+                *reinterpret_cast<uint4*>(qt_row + ((c ^ (r & 7)) << 4)) = make_uint4(word[0], word[1], word[2], word[3]);
             }
+            fence_proxy_async_smem();
+            named_barrier_sync(kQBarrier, kQThreads);
         }
         float slope2 = 0.f, cap2 = 0.f, inv_cap = 0.f;
         if constexpr (MODS) {
@@ -520,6 +533,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         uint64_t* my_dec = decided + grp * 4 + quarter;
         uint64_t* their_dec = decided + (grp ^ 1) * 4 + quarter;
         bool stop = false;
+        int slot = 0, turn = 0;  // i % kSlots, i / kSlots
         // The unit's block entry is read one pair ahead; (n_blk, n_sub) walk the
         // group's units without a division.
         int n_blk = grp / upb, n_sub = grp % upb;
@@ -544,8 +558,8 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
             const bool warp_any = __any_sync(0xffffffffu, mine);
             const float ks = __uint_as_float(info.z);
             const float lv = __uint_as_float(info.w);  // log2 of the v scale
-            const uint32_t scol = lane_addr + kColS + (u & 3) * 64;
-            if (!mbar_wait(&sfull[i & 1], (i >> 1) & 1)) {
+            const uint32_t scol = lane_addr + kColS + slot * 128 + grp * 64;
+            if (!mbar_wait(&sfull[slot], turn & 1)) {
                 *s_abort = 1;
                 stop = true;
             }
@@ -564,29 +578,54 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                     for (int e = 0; e < 64; ++e) xs[e] = __uint_as_float(sv[e]);
                     if (a.cap > 0.f) {
                         const float um = mul * inv_cap;
-                        float big = 0.f;
+                        float pa[4], pi[4];
 #pragma unroll
-                        for (int e = 0; e < 64; ++e) big = fmaxf(big, fabsf(xs[e]));
-                        if (__any_sync(0xffffffffu, mine && !(big * fabsf(um) <= kTanhSmall))) {
+                        for (int k = 0; k < 4; ++k) pa[k] = pi[k] = xs[k];
 #pragma unroll
-                            for (int e = 0; e < 64; ++e) xs[e] = cap2 * q8_tanh(xs[e] * um);
-                        } else {
-                            // every |u| is small: the polynomial on packed pairs
-                            const float2 um2 = make_float2(um, um), c2 = make_float2(cap2, cap2);
-                            const float2 z2 = make_float2(0.f, 0.f);
+                        for (int e = 4; e < 64; e += 2) {
+                            pa[(e >> 1) & 3] = fmax3(pa[(e >> 1) & 3], xs[e], xs[e + 1]);
+                            pi[(e >> 1) & 3] = fmin3(pi[(e >> 1) & 3], xs[e], xs[e + 1]);
+                        }
+                        const float big = fmaxf(fmaxf(fmaxf(pa[0], pa[1]), fmaxf(pa[2], pa[3])),
+                                                -fminf(fminf(pi[0], pi[1]), fminf(pi[2], pi[3]))) * fabsf(um);
+                        // cap2 * tanh(S * um) = S * (A + v * (B0 + v * (B1 + ...))), v = S^2, as long
+                        // as every |u| of the warp is small; on packed pairs
+                        const float A = um * cap2, um2 = um * um;
+                        const float2 z2 = make_float2(0.f, 0.f), A2 = make_float2(A, A);
+                        if (!__any_sync(0xffffffffu, mine && !(big <= kTanhTiny))) {
+                            const float b0 = A * um2, b1 = b0 * um2, b2 = b1 * um2;
+                            const float2 B0 = make_float2(b0 * kTanhT0, b0 * kTanhT0);
+                            const float2 B1 = make_float2(b1 * kTanhT1, b1 * kTanhT1);
+                            const float2 B2 = make_float2(b2 * kTanhT2, b2 * kTanhT2);
 #pragma unroll
                             for (int e = 0; e < 64; e += 2) {
-                                const float2 x = ffma2(make_float2(xs[e], xs[e + 1]), um2, z2);
+                                const float2 x = make_float2(xs[e], xs[e + 1]);
                                 const float2 v = ffma2(x, x, z2);
-                                float2 p = ffma2(v, make_float2(kTanhC4, kTanhC4), make_float2(kTanhC3, kTanhC3));
-                                p = ffma2(v, p, make_float2(kTanhC2, kTanhC2));
-                                p = ffma2(v, p, make_float2(kTanhC1, kTanhC1));
-                                p = ffma2(v, p, make_float2(kTanhC0, kTanhC0));
-                                const float2 t = ffma2(ffma2(x, v, z2), p, x);
-                                const float2 y = ffma2(t, c2, z2);
+                                const float2 t = ffma2(v, ffma2(v, ffma2(v, B2, B1), B0), A2);
+                                const float2 y = ffma2(x, t, z2);
                                 xs[e] = y.x;
                                 xs[e + 1] = y.y;
                             }
+                        } else if (!__any_sync(0xffffffffu, mine && !(big <= kTanhSmall))) {
+                            const float b0 = A * um2, b1 = b0 * um2, b2 = b1 * um2, b3 = b2 * um2, b4 = b3 * um2;
+                            const float2 B0 = make_float2(b0 * kTanhC0, b0 * kTanhC0);
+                            const float2 B1 = make_float2(b1 * kTanhC1, b1 * kTanhC1);
+                            const float2 B2 = make_float2(b2 * kTanhC2, b2 * kTanhC2);
+                            const float2 B3 = make_float2(b3 * kTanhC3, b3 * kTanhC3);
+                            const float2 B4 = make_float2(b4 * kTanhC4, b4 * kTanhC4);
+#pragma unroll
+                            for (int e = 0; e < 64; e += 2) {
+                                const float2 x = make_float2(xs[e], xs[e + 1]);
+                                const float2 v = ffma2(x, x, z2);
+                                float2 t = ffma2(v, ffma2(v, B4, B3), B2);
+                                t = ffma2(v, ffma2(v, ffma2(v, t, B1), B0), A2);
+                                const float2 y = ffma2(x, t, z2);
+                                xs[e] = y.x;
+                                xs[e + 1] = y.y;
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 64; ++e) xs[e] = cap2 * q8_tanh(xs[e] * um);
                         }
                     } else {
                         const float m2 = mul * kLog2e;
@@ -666,7 +705,8 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
             if (__any_sync(0xffffffffu, corr != 1.f)) {
                 // O holds earlier units of these rows: rescale once the previous
                 // unit's P V has landed
-                if (!mbar_wait(&obar[(u - 1) & 3], ((u - 1) >> 2) & 1)) *s_abort = 1;
+                const int before = grp == 1 ? 2 * slot : (slot == 0 ? 2 * kSlots - 1 : 2 * slot - 1);
+                if (!mbar_wait(&obar[before], (grp == 0 && slot == 0 ? turn - 1 : turn) & 1)) *s_abort = 1;
                 tc_fence_after();
 #pragma unroll 1
                 for (int ch = 0; ch < 4; ++ch) {
@@ -694,7 +734,11 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&pfull[u & 3]);
+            if (lane == 0) mbar_arrive(&pfull[2 * slot + grp]);
+            if (++slot == kSlots) {
+                slot = 0;
+                ++turn;
+            }
         }
         // ---------------- epilogue: O / l -> bf16, 64 dims per group ----------------
         named_barrier_sync(kEndBarrier, kEndThreads);  // both groups' references are final

@@ -229,6 +229,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     return d;
 }
 
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Packed fp32 pairs (sm_100): a * b + c and a + b on both lanes of a float2 in
 // one instruction each, round to nearest.
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
