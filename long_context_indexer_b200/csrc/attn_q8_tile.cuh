@@ -124,6 +124,22 @@ __device__ __forceinline__ void split_weights(float a, float b, float c, float d
     lo = f16x4_to_e4m3(*reinterpret_cast<const uint32_t*>(&r0), *reinterpret_cast<const uint32_t*>(&r1));
 }
 
+// Waits for a barrier's phase. A wait that runs out makes the tile give up:
+// every further wait of the tile returns at once and its rows become zero.
+__device__ __forceinline__ void tile_wait(uint64_t* bar, uint32_t parity, volatile int* s_abort) {
+    if (mbar_try_wait(bar, parity)) return;
+    const unsigned long long t0 = global_ns();
+    const unsigned long long limit = g_wait_limit_ns;
+    while (!mbar_try_wait(bar, parity)) {
+        if (*s_abort) return;
+        if (global_ns() - t0 > limit) {
+            raise_status(kStatusTimeout);
+            *s_abort = 1;
+            return;
+        }
+    }
+}
+
 // One query row and head by one warp, fp32, reading only attended tokens
 // (sq: hd floats of shared memory of this warp).
 __device__ __noinline__ void q8_row_by_warp(const AttnQ8Args& a, int row, int h, float* sq) {
@@ -532,44 +548,53 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         float l = 0.f;        // this group's share of the row sum, relative to m
         uint64_t* my_dec = decided + grp * 4 + quarter;
         uint64_t* their_dec = decided + (grp ^ 1) * 4 + quarter;
-        bool stop = false;
         int slot = 0, turn = 0;  // i % kSlots, i / kSlots
-        // The unit's block entry is read one pair ahead; (n_blk, n_sub) walk the
-        // group's units without a division.
+        // The group's units in order, (n_blk, n_sub) without a division; what the
+        // row sees of a unit is worked out one unit ahead.
         int n_blk = grp / upb, n_sub = grp % upb;
-        uint4 n_info = uinfo[min(n_blk, kMaxUnion - 1)];
-        for (int i = 0; i < npairs; ++i) {
-            const int u = 2 * i + grp;
-            const uint4 info = n_info;
-            const int t0 = (int)info.x + n_sub * kUnit;                    // its first token
-            const bool there = u < nunits && info.x != ~0u;
+        float ks = 0.f, lv = 0.f;    // k scale, log2 of the v scale
+        int t0 = 0, lo = 0, hi = -1;  // first token; attended columns lo .. hi
+        bool there = false, warp_any = false;
+        auto look = [&](int u) {
+            const uint4 info = uinfo[min(n_blk, kMaxUnion - 1)];
+            t0 = (int)info.x + n_sub * kUnit;
+            there = u < nunits && info.x != ~0u;
+            ks = __uint_as_float(info.z);
+            lv = __uint_as_float(info.w);
+            lo = 0;
+            hi = -1;
+            if (there && (info.y & qbit) != 0u) {
+                lo = max(win.lo - t0, 0);
+                hi = min(win.hi - t0, kUnit - 1);
+            }
+            warp_any = __any_sync(0xffffffffu, hi >= lo);
             n_sub += 2;
             while (n_sub >= upb) {
                 n_sub -= upb;
                 ++n_blk;
             }
-            n_info = uinfo[min(n_blk, kMaxUnion - 1)];
-            int lo = 0, hi = -1;  // attended columns lo .. hi
-            if (there && (info.y & qbit) != 0u) {
-                lo = max(win.lo - t0, 0);
-                hi = min(win.hi - t0, kUnit - 1);
-            }
+        };
+        look(grp);
+        for (int i = 0; i < npairs; ++i) {
             const bool mine = hi >= lo;
-            const bool warp_any = __any_sync(0xffffffffu, mine);
-            const float ks = __uint_as_float(info.z);
-            const float lv = __uint_as_float(info.w);  // log2 of the v scale
             const uint32_t scol = lane_addr + kColS + slot * 128 + grp * 64;
-            if (!mbar_wait(&sfull[slot], turn & 1)) {
-                *s_abort = 1;
-                stop = true;
-            }
-            if (*s_abort) stop = true;
-            stop = __any_sync(0xffffffffu, stop);
+            if (!warp_any) {
+                // nothing of the unit concerns these rows: pass the references on, P = 0
+                if (grp == 1 || i > 0) tile_wait(their_dec, (grp == 1 ? i : i - 1) & 1, s_abort);
+                if (lane == 0) mbar_arrive(my_dec);
+                tile_wait(&sfull[slot], turn & 1, s_abort);
+                tc_fence_after();
+                uint32_t none[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) none[e] = 0u;
+                tmem_st32(scol, none);
+            } else {
+            tile_wait(&sfull[slot], turn & 1, s_abort);
             tc_fence_after();
             float mx = -INFINITY;
             float mul = unit * ks;
             uint32_t sv[64];
-            if (warp_any && !stop) {
+            {
                 tmem_ld64(scol, sv);
                 if constexpr (MODS) {
                     // raw S -> capped, biased logits in log2 units; then mul = 1
@@ -656,27 +681,24 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                 mx = mine ? mx * mul + lv : -INFINITY;
             }
             // the reference after the unit before this one, then after this one
-            if (grp == 1 || i > 0) {
-                if (!stop && !mbar_wait(their_dec, grp == 1 ? i & 1 : (i - 1) & 1)) {
-                    *s_abort = 1;
-                    stop = true;
-                }
-                stop = __any_sync(0xffffffffu, stop);
-            }
-            if (stop) break;
+            if (grp == 1 || i > 0) tile_wait(their_dec, (grp == 1 ? i : i - 1) & 1, s_abort);
             const float m_in = mref[r];
-            if (m_in != m) {
-                l *= fast_exp2(m - m_in);  // m = -inf: nothing summed yet
+            float corr = 1.f;
+            const bool moves = mx > m_in + kLazy;
+            const bool any_moves = __any_sync(0xffffffffu, moves);  // and every lane has read mref
+            if (__any_sync(0xffffffffu, m_in != m)) {
+                l *= m_in != m ? fast_exp2(m - m_in) : 1.f;  // m = -inf: nothing summed yet
                 m = m_in;
             }
-            float corr = 1.f;
-            if (mx > m + kLazy) {
-                if (m > -INFINITY) corr = fast_exp2(m - mx);
-                l *= corr;
-                m = mx;
-                mref[r] = m;
+            if (any_moves) {
+                if (moves) {
+                    if (m > -INFINITY) corr = fast_exp2(m - mx);
+                    l *= corr;
+                    m = mx;
+                    mref[r] = m;
+                }
+                __syncwarp();
             }
-            __syncwarp();
             if (lane == 0) mbar_arrive(my_dec);
             uint32_t pk[32];  // 16 words of high parts, 16 of low parts
             if (mine) {
@@ -702,11 +724,11 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                 for (int e = 0; e < 32; ++e) pk[e] = 0u;
             }
             tmem_st32(scol, pk);
-            if (__any_sync(0xffffffffu, corr != 1.f)) {
+            if (any_moves && __any_sync(0xffffffffu, corr != 1.f)) {
                 // O holds earlier units of these rows: rescale once the previous
                 // unit's P V has landed
                 const int before = grp == 1 ? 2 * slot : (slot == 0 ? 2 * kSlots - 1 : 2 * slot - 1);
-                if (!mbar_wait(&obar[before], (grp == 0 && slot == 0 ? turn - 1 : turn) & 1)) *s_abort = 1;
+                tile_wait(&obar[before], (grp == 0 && slot == 0 ? turn - 1 : turn) & 1, s_abort);
                 tc_fence_after();
 #pragma unroll 1
                 for (int ch = 0; ch < 4; ++ch) {
@@ -717,12 +739,13 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                     tmem_st32(lane_addr + kColO + ch * 32, ov);
                 }
             }
+            }
             tmem_wait_st();
             // V rows of tokens past the context and of absent units must be zero
             // before the MMA reads them (this thread: half of row r / 2 of the unit)
             if (!there || t0 > ctx32 - kUnit) {
                 const int vs = i & (kStages - 1);
-                if (!mbar_wait(&vfull[vs], (i / kStages) & 1)) *s_abort = 1;
+                tile_wait(&vfull[vs], (i / kStages) & 1, s_abort);
                 const int vr = r >> 1;
                 if (!there || t0 + vr >= ctx32) {
                     unsigned char* vt = smem + kOffV + vs * kStageBytes + grp * kUnitBytes + vr * 128;
@@ -739,6 +762,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                 slot = 0;
                 ++turn;
             }
+            look(2 * (i + 1) + grp);
         }
         // ---------------- epilogue: O / l -> bf16, 64 dims per group ----------------
         named_barrier_sync(kEndBarrier, kEndThreads);  // both groups' references are final
@@ -746,9 +770,9 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         if (m_end != m) l *= fast_exp2(m - m_end);
         lsum[grp * 128 + r] = l;
         named_barrier_sync(kEndBarrier, kEndThreads);
-        const float L = lsum[r] + lsum[128 + r];
-        if (!mbar_wait(drain, 0)) *s_abort = 1;
+        tile_wait(drain, 0, s_abort);
         tc_fence_after();
+        const float L = *s_abort ? 0.f : lsum[r] + lsum[128 + r];
         const float inv = 1.f / L;
         if (a.lse && real && grp == 0) a.lse[qrow] = L == 0.f ? -INFINITY : m_end - kShift + log2f(L);
         __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) + qrow * kHD + grp * 64;
