@@ -27,7 +27,9 @@
 // passes it by more than 3.75 (weights stay below 448), and O is rescaled only
 // then.
 //
-// Warps: 0 TMA producer, 1 MMA issuer, 2..5 and 6..9 two softmax groups that
+// Warps: 0 TMA producer, 1 issues Q K^T, 2 issues P V (the waits and commits
+// around the one hide behind the MMAs of the other; from one thread they left
+// the tensor pipe idle half of the time), 3..6 and 7..10 two softmax groups that
 // take the even and the odd units, one thread per row. A warp (two queries at
 // 16 heads) none of whose queries selected the unit skips its loads and
 // exponentials, so with sparse selections the groups work ahead of each other
@@ -62,7 +64,8 @@ constexpr int kStages = 4;             // a power of two
 constexpr int kMaxWords = 512;         // block bitmap words: nb_max <= 16384
 constexpr int kMaxUnion = 2048;        // distinct blocks per tile
 constexpr int kGroupWarps = 4;
-constexpr int kThreads = 64 + 2 * 32 * kGroupWarps;
+constexpr int kFirstSoftmax = 3;       // warps 0..2: TMA, Q K^T, P V
+constexpr int kThreads = 32 * kFirstSoftmax + 2 * 32 * kGroupWarps;
 constexpr int kSlots = 3;              // pairs of S in flight
 // TMEM columns: O fp32, kSlots pairs of S (fp32; a unit's 64 columns then hold
 // its P as 16 columns of high and 16 of low parts)
@@ -216,13 +219,13 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
     uint64_t* sfull = vempty + kStages;      // [kSlots] a pair's S written
     uint64_t* pfull = sfull + kSlots;        // [2 * kSlots] a unit's P written (4 warps)
     uint64_t* decided = pfull + 2 * kSlots;  // [2][4] a group's reference of a unit, per 32 rows
-    uint64_t* obar = decided + 8;            // [2 * kSlots] a unit's P V completed
-    uint64_t* drain = obar + 2 * kSlots;     // every MMA of the tile completed
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* obar = decided + 8;            // [kSlots] P V of a pair's first unit completed
+    uint64_t* drain = obar + kSlots;         // [2] every MMA of an issuer completed
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
     int* s_nunion = reinterpret_cast<int*>(tmem_slot + 1);
     // set by any role whose bounded wait ran out: every role then stops
     volatile int* s_abort = s_nunion + 1;
-    static_assert((4 * kStages + 5 * kSlots + 8 + 1) * 8 + 12 <= 512, "barriers fit");
+    static_assert((4 * kStages + 4 * kSlots + 8 + 2) * 8 + 12 <= 512, "barriers fit");
     float* mref = reinterpret_cast<float*>(smem + kOffRow);  // [128]
     float* lsum = mref + 128;                                // [2][128]
     int* redo = reinterpret_cast<int*>(lsum + 256);          // [128]
@@ -247,13 +250,13 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
             mbar_init(&vfull[i], 1);
             mbar_init(&vempty[i], 1);
         }
-        for (int i = 0; i < kSlots; ++i) mbar_init(&sfull[i], 1);
-        for (int i = 0; i < 2 * kSlots; ++i) {
-            mbar_init(&pfull[i], kGroupWarps);
+        for (int i = 0; i < kSlots; ++i) {
+            mbar_init(&sfull[i], 1);
             mbar_init(&obar[i], 1);
         }
+        for (int i = 0; i < 2 * kSlots; ++i) mbar_init(&pfull[i], kGroupWarps);
         for (int i = 0; i < 8; ++i) mbar_init(&decided[i], 1);
-        mbar_init(drain, 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
         *s_abort = 0;
         fence_mbar_init();
     }
@@ -398,8 +401,8 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                 issued = i + 1;
                 for (int kv = 0; kv < 2 && ok; ++kv) {
                     uint64_t* full = kv ? &vfull[st] : &kfull[st];
-                    if (*s_abort || (i >= kStages && !mbar_wait(kv ? &vempty[st] : &kempty[st], ph))) {
-                        *s_abort = 1;
+                    if (i >= kStages) tile_wait(kv ? &vempty[st] : &kempty[st], ph, s_abort);
+                    if (*s_abort) {
                         ok = false;
                         break;
                     }
@@ -416,43 +419,22 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
             }
         }
     } else if (warp == 1) {
-        // ---------------- MMA issuer ----------------
+        // ---------------- S = Q K^T ----------------
         named_barrier_sync(kQBarrier, kQThreads);
         tc_fence_after();
         if (lane == 0) {
             // operand descriptors of stage 0; a stage is 1024 units of 16 bytes on
             const uint64_t kd0 = sw128_desc(smem_u32(smem + kOffK));
-            const uint64_t vd0 = sw128_desc_mn(smem_u32(smem + kOffV), kUnitBytes);
             const uint64_t qd0 = sw128_desc(smem_u32(smem + kOffQ));
-            const uint32_t o_col = tmem_base + kColO;
-            bool fine = true;
-            auto pv = [&](int j) {
-                const int vs = j & (kStages - 1), slot = j % kSlots;
-                fine = fine && mbar_wait(&vfull[vs], (j / kStages) & 1);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    fine = fine && mbar_wait(&pfull[2 * slot + c], (j / kSlots) & 1);
-                    if (!fine) break;
-                    tc_fence_after();
-                    const uint32_t p = tmem_base + kColS + slot * 128 + c * 64;
-                    const uint64_t vd = vd0 + (uint32_t)(vs * (kStageBytes >> 4) + c * (kUnitBytes >> 4));
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int kt = 0; kt < kUnit / 32; ++kt)
-                            tc_mma_f8_tmem_a(o_col, p + part * 16 + kt * 8, vd + kt * (4096 >> 4), kIdescPV,
-                                             (j | c | part | kt) != 0 ? 1u : 0u);
-                    tc_commit(&obar[2 * slot + c]);
-                }
-                if (fine) tc_commit(&vempty[vs]);
-            };
-            for (int i = 0; i < npairs && fine; ++i) {
+            for (int i = 0; i < npairs; ++i) {
                 const int ks = i & (kStages - 1);
-                fine = mbar_wait(&kfull[ks], (i / kStages) & 1) && !*s_abort;
-                if (!fine) break;
+                tile_wait(&kfull[ks], (i / kStages) & 1, s_abort);
+                // the slot's last pair has had its P V done
+                const int j = i - kSlots;
+                if (j >= 0) tile_wait(&vempty[j & (kStages - 1)], (j / kStages) & 1, s_abort);
+                if (*s_abort) break;
                 tc_fence_after();
                 const uint64_t kd = kd0 + (uint32_t)(ks * (kStageBytes >> 4));
-                // the slot's last pair, i - kSlots, has had its P V issued
                 const uint32_t d = tmem_base + kColS + (i % kSlots) * 128;
 #pragma unroll
                 for (int part = 0; part < 2; ++part)
@@ -462,18 +444,44 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                                   (part | kk) != 0 ? 1u : 0u);
                 tc_commit(&sfull[i % kSlots]);
                 tc_commit(&kempty[ks]);
-                if (i >= kSlots - 1) pv(i - (kSlots - 1));
             }
-            for (int j = max(0, npairs - (kSlots - 1)); j < npairs && fine; ++j) pv(j);
-            if (!fine) *s_abort = 1;
             // nothing of this thread may still run on the tensor core when the
-            // TMEM is released; the epilogue waits for it too
-            tc_commit(drain);
-            mbar_wait(drain, 0);
+            // TMEM is released
+            tc_commit(&drain[0]);
+            mbar_wait(&drain[0], 0);
+        }
+    } else if (warp == 2) {
+        // ---------------- O += P V ----------------
+        if (lane == 0) {
+            const uint64_t vd0 = sw128_desc_mn(smem_u32(smem + kOffV), kUnitBytes);
+            const uint32_t o_col = tmem_base + kColO;
+            for (int j = 0; j < npairs; ++j) {
+                const int vs = j & (kStages - 1), slot = j % kSlots;
+                tile_wait(&vfull[vs], (j / kStages) & 1, s_abort);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    tile_wait(&pfull[2 * slot + c], (j / kSlots) & 1, s_abort);
+                    if (*s_abort) break;
+                    tc_fence_after();
+                    const uint32_t p = tmem_base + kColS + slot * 128 + c * 64;
+                    const uint64_t vd = vd0 + (uint32_t)(vs * (kStageBytes >> 4) + c * (kUnitBytes >> 4));
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int kt = 0; kt < kUnit / 32; ++kt)
+                            tc_mma_f8_tmem_a(o_col, p + part * 16 + kt * 8, vd + kt * (4096 >> 4), kIdescPV,
+                                             (j | c | part | kt) != 0 ? 1u : 0u);
+                    if (c == 0) tc_commit(&obar[slot]);
+                }
+                if (*s_abort) break;
+                tc_commit(&vempty[vs]);
+            }
+            tc_commit(&drain[1]);  // the epilogue waits for it too
+            mbar_wait(&drain[1], 0);
         }
     } else {
         // ---------------- softmax and epilogue: a thread per row and group ----------------
-        const int grp = (warp - 2) >> 2;  // units 2i + grp
+        const int grp = (warp - kFirstSoftmax) >> 2;  // units 2i + grp
         const int quarter = warp & 3;     // TMEM lanes of this warp
         const int r = quarter * 32 + lane;
         const int qi = r / G, s = s0 + qi;
@@ -727,8 +735,10 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
             if (any_moves && __any_sync(0xffffffffu, corr != 1.f)) {
                 // O holds earlier units of these rows: rescale once the previous
                 // unit's P V has landed
-                const int before = grp == 1 ? 2 * slot : (slot == 0 ? 2 * kSlots - 1 : 2 * slot - 1);
-                tile_wait(&obar[before], (grp == 0 && slot == 0 ? turn - 1 : turn) & 1, s_abort);
+                if (grp == 1)
+                    tile_wait(&obar[slot], turn & 1, s_abort);
+                else
+                    tile_wait(&vempty[(i - 1) & (kStages - 1)], ((i - 1) / kStages) & 1, s_abort);
                 tc_fence_after();
 #pragma unroll 1
                 for (int ch = 0; ch < 4; ++ch) {
@@ -770,7 +780,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         if (m_end != m) l *= fast_exp2(m - m_end);
         lsum[grp * 128 + r] = l;
         named_barrier_sync(kEndBarrier, kEndThreads);
-        tile_wait(drain, 0, s_abort);
+        tile_wait(&drain[1], 0, s_abort);
         tc_fence_after();
         const float L = *s_abort ? 0.f : lsum[r] + lsum[128 + r];
         const float inv = 1.f / L;
