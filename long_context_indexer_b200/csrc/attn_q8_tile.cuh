@@ -28,14 +28,12 @@
 // then.
 //
 // Warps: 0 TMA producer, 1 issues Q K^T, 2 issues P V (the waits and commits
-// around the one hide behind the MMAs of the other; from one thread they left
-// the tensor pipe idle half of the time), 3..6 and 7..10 two softmax groups that
-// take the even and the odd units, one thread per row. A warp (two queries at
-// 16 heads) none of whose queries selected the unit skips its loads and
-// exponentials, so with sparse selections the groups work ahead of each other
-// and the tensor pipe sets the pace (1028 cycles a pair). The groups agree on a
-// row's reference in unit order: a short chain of one mbarrier per 32 rows and
-// group, between the maximum and the exponentials of each unit.
+// around the one hide behind the MMAs of the other), then three softmax groups of
+// four warps that take every third unit, one thread per row. A warp (two queries
+// at 16 heads) none of whose queries selected the unit only stores zero weights,
+// so with sparse selections the warps work ahead of each other. The groups agree
+// on a row's reference in unit order: a short chain of one mbarrier per 32 rows
+// and group, between the maximum and the exponentials of each unit.
 //
 // Unset memory and NaN. Units past the context, and V rows behind the last
 // token, never reach the MMA (skipped, or zeroed in shared memory). A NaN code
@@ -63,9 +61,10 @@ constexpr int kStageBytes = 2 * kUnitBytes;  // a pair: 16 KiB of K or of V
 constexpr int kStages = 4;             // a power of two
 constexpr int kMaxWords = 512;         // block bitmap words: nb_max <= 16384
 constexpr int kMaxUnion = 2048;        // distinct blocks per tile
+constexpr int kGroups = 3;             // softmax groups, unit u belongs to group u % kGroups
 constexpr int kGroupWarps = 4;
 constexpr int kFirstSoftmax = 3;       // warps 0..2: TMA, Q K^T, P V
-constexpr int kThreads = 32 * kFirstSoftmax + 2 * 32 * kGroupWarps;
+constexpr int kThreads = 32 * kFirstSoftmax + kGroups * 32 * kGroupWarps;
 constexpr int kSlots = 3;              // pairs of S in flight
 // TMEM columns: O fp32, kSlots pairs of S (fp32; a unit's 64 columns then hold
 // its P as 16 columns of high and 16 of low parts)
@@ -80,8 +79,8 @@ constexpr int kOffUnion = kOffQ + 2 * kRows * kHD;
 constexpr int kUnionBytes = 2 * kMaxWords * 4 + kMaxUnion * (16 + 4);
 constexpr int kOffWin = kOffUnion + kUnionBytes;    // [kMaxQT] Q8Window
 constexpr int kOffBar = kOffWin + kMaxQT * 16;
-constexpr int kOffRow = kOffBar + 512;              // [128] references, [2][128] sums, [128] flags
-constexpr int kSmemBytes = kOffRow + 4 * 128 * 4 + 1024 /*alignment slack*/;
+constexpr int kOffRow = kOffBar + 512;              // [128] references, [kGroups][128] sums, [128] flags, [128] factors
+constexpr int kSmemBytes = kOffRow + (3 + kGroups) * 128 * 4 + 1024 /*alignment slack*/;
 // instruction descriptors, kind::f8f6f4: D fp32, A and B e4m3, M = 128, N = 128
 constexpr uint32_t kIdescQK = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);  // B MN-major
@@ -218,17 +217,18 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
     uint64_t* vempty = vfull + kStages;    // [kStages]
     uint64_t* sfull = vempty + kStages;      // [kSlots] a pair's S written
     uint64_t* pfull = sfull + kSlots;        // [2 * kSlots] a unit's P written (4 warps)
-    uint64_t* decided = pfull + 2 * kSlots;  // [2][4] a group's reference of a unit, per 32 rows
-    uint64_t* obar = decided + 8;            // [kSlots] P V of a pair's first unit completed
+    uint64_t* decided = pfull + 2 * kSlots;  // [kGroups][4] a group's reference of a unit, per 32 rows
+    uint64_t* obar = decided + 4 * kGroups;  // [kSlots] P V of a pair's first unit completed
     uint64_t* drain = obar + kSlots;         // [2] every MMA of an issuer completed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
     int* s_nunion = reinterpret_cast<int*>(tmem_slot + 1);
-    // set by any role whose bounded wait ran out: every role then stops
+    // set by any role whose bounded wait ran out: the tile then gives up
     volatile int* s_abort = s_nunion + 1;
-    static_assert((4 * kStages + 4 * kSlots + 8 + 2) * 8 + 12 <= 512, "barriers fit");
+    static_assert((4 * kStages + 4 * kSlots + 4 * kGroups + 2) * 8 + 12 <= 512, "barriers fit");
     float* mref = reinterpret_cast<float*>(smem + kOffRow);  // [128]
-    float* lsum = mref + 128;                                // [2][128]
-    int* redo = reinterpret_cast<int*>(lsum + 256);          // [128]
+    float* lsum = mref + 128;                                // [kGroups][128]
+    int* redo = reinterpret_cast<int*>(lsum + kGroups * 128);  // [128]
+    float* rowmul = reinterpret_cast<float*>(redo + 128);      // [128] inverse of a query row's factor
 
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
             mbar_init(&obar[i], 1);
         }
         for (int i = 0; i < 2 * kSlots; ++i) mbar_init(&pfull[i], kGroupWarps);
-        for (int i = 0; i < 8; ++i) mbar_init(&decided[i], 1);
+        for (int i = 0; i < 4 * kGroups; ++i) mbar_init(&decided[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&drain[i], 1);
         *s_abort = 0;
         fence_mbar_init();
@@ -290,6 +290,48 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         redo[tid] = 0;
     }
     __syncthreads();
+    // ---- query rows -> shared memory, a warp per row (coalesced), beside the
+    // union: scaled so that the largest element is in [2^7, 2^8), high and low parts ----
+    if (warp >= kFirstSoftmax) {
+        constexpr int kQWarps = kGroups * kGroupWarps, kQRows = (kRows + kQWarps - 1) / kQWarps;
+        const int w0 = warp - kFirstSoftmax;
+        uint2 q4[kQRows];
+#pragma unroll
+        for (int k = 0; k < kQRows; ++k) {
+            const int r = w0 + k * kQWarps, qi = r / G;
+            const bool real = r < QT * G && s0 + qi < a.S;
+            const size_t at = (((size_t)b * a.S + s0 + qi) * a.H_q + (size_t)g * G + (r - qi * G)) * kHD + 4 * lane;
+            q4[k] = real ? __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + at))
+                         : make_uint2(0u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < kQRows; ++k) {
+            const int r = w0 + k * kQWarps;
+            if (r >= kRows) break;
+            float2 f0 = bf16x2_to_f32(q4[k].x), f1 = bf16x2_to_f32(q4[k].y);
+            const float amax = warp_max(fmaxf(fmaxf(fabsf(f0.x), fabsf(f0.y)), fmaxf(fabsf(f1.x), fabsf(f1.y))));
+            // a row with an infinity or a NaN is computed apart
+            const float sum = f0.x + f0.y + f1.x + f1.y;
+            if (__any_sync(0xffffffffu, !(fabsf(sum) <= 3.402823466e38f)) && lane == 0) redo[r] = 1;
+            int e = (int)(__float_as_uint(amax) >> 23) - 127;
+            e = e < -100 ? -100 : e > 127 ? 127 : e;
+            const float up = __uint_as_float((uint32_t)(7 - e + 127) << 23);
+            if (lane == 0) rowmul[r] = __uint_as_float((uint32_t)(e - 7 + 127) << 23);
+            f0.x *= up;
+            f0.y *= up;
+            f1.x *= up;
+            f1.y *= up;
+            const uint32_t hi = f32_to_e4m3x4(f0.x, f0.y, f1.x, f1.y);
+            float back[4];
+            e4m3x4_to_f32(hi, back);
+            const uint32_t lo = f32_to_e4m3x4(f0.x - back[0], f0.y - back[1], f1.x - back[2], f1.y - back[3]);
+            // byte 4 * lane of the row, 16-byte chunks swizzled
+            unsigned char* d = smem + kOffQ + r * kHD + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3);
+            *reinterpret_cast<uint32_t*>(d) = hi;
+            *reinterpret_cast<uint32_t*>(d + kRows * kHD) = lo;
+        }
+        fence_proxy_async_smem();
+    }
     // block of entry e if its query can attend a token of it, else -1
     auto entry = [&](int e, int qi) -> int {
         const int j = e == tid ? j_mine : __ldg(tile_ids + e);
@@ -372,10 +414,8 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    // named barrier 1: the MMA warp waits for the query rows in shared memory;
-    // named barrier 2: the softmax warps before the epilogue
-    constexpr int kQBarrier = 1, kQThreads = 32 + 64 * kGroupWarps;
-    constexpr int kEndBarrier = 2, kEndThreads = 64 * kGroupWarps;
+    // named barrier: the softmax warps before the epilogue
+    constexpr int kEndBarrier = 1, kEndThreads = 32 * kGroups * kGroupWarps;
 
     int issued = 0;  // pairs whose copies the producer thread started
     if (warp == 0) {
@@ -420,8 +460,6 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         }
     } else if (warp == 1) {
         // ---------------- S = Q K^T ----------------
-        named_barrier_sync(kQBarrier, kQThreads);
-        tc_fence_after();
         if (lane == 0) {
             // operand descriptors of stage 0; a stage is 1024 units of 16 bytes on
             const uint64_t kd0 = sw128_desc(smem_u32(smem + kOffK));
@@ -481,7 +519,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         }
     } else {
         // ---------------- softmax and epilogue: a thread per row and group ----------------
-        const int grp = (warp - kFirstSoftmax) >> 2;  // units 2i + grp
+        const int grp = (warp - kFirstSoftmax) >> 2;
         const int quarter = warp & 3;     // TMEM lanes of this warp
         const int r = quarter * 32 + lane;
         const int qi = r / G, s = s0 + qi;
@@ -492,58 +530,8 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         const Q8Window win = wins[min(qi, kMaxQT - 1)];
         const uint32_t lane_addr = tmem_base + ((uint32_t)(quarter * 32) << 16);
         const int ctx32 = (int)(ctx < 0x7fffffffLL ? ctx : 0x7fffffffLL);
-        float unit = MODS ? a.scale : a.scale * kLog2e;  // what raw S is multiplied by, with the k scale
-        // ---- query row -> shared memory: group 0 stores the high parts, group 1 the low ----
-        {
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + qrow * kHD);
-            float amax = 0.f;
-            bool odd = false;  // not finite
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const uint4 w = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 f = bf16x2_to_f32(x[k]);
-                    amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-                    odd = odd || f.x != f.x || f.y != f.y;
-                }
-            }
-            odd = odd || amax > 3.402823466e38f;
-            if (odd) redo[r] = 1;  // such a row is computed apart
-            int e = (int)(__float_as_uint(amax) >> 23) - 127;
-            e = e < -100 ? -100 : e > 127 ? 127 : e;
-            const float up = __uint_as_float((uint32_t)(7 - e + 127) << 23);  // largest element in [2^7, 2^8)
-            unit *= __uint_as_float((uint32_t)(e - 7 + 127) << 23);
-            unsigned char* qt_row = smem + kOffQ + grp * (kRows * kHD) + r * kHD;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {  // 16 dims; again from L1: the row is not held
-                uint32_t word[4];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint4 w = real ? __ldg(src + 2 * c + k) : make_uint4(0, 0, 0, 0);
-                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        float2 f0 = bf16x2_to_f32(x[2 * n]), f1 = bf16x2_to_f32(x[2 * n + 1]);
-                        f0.x *= up;
-                        f0.y *= up;
-                        f1.x *= up;
-                        f1.y *= up;
-                        uint32_t codes = f32_to_e4m3x4(f0.x, f0.y, f1.x, f1.y);
-                        if (grp == 1) {
-                            float hi[4];
-                            e4m3x4_to_f32(codes, hi);
-                            codes = f32_to_e4m3x4(f0.x - hi[0], f0.y - hi[1], f1.x - hi[2], f1.y - hi[3]);
-                        }
-                        word[2 * k + n] = codes;
-                    }
-                }
-                *reinterpret_cast<uint4*>(qt_row + ((c ^ (r & 7)) << 4)) = make_uint4(word[0], word[1], word[2], word[3]);
-            }
-            fence_proxy_async_smem();
-            named_barrier_sync(kQBarrier, kQThreads);
-        }
+        // what raw S is multiplied by, with the k scale
+        const float unit = (MODS ? a.scale : a.scale * kLog2e) * rowmul[r];
         float slope2 = 0.f, cap2 = 0.f, inv_cap = 0.f;
         if constexpr (MODS) {
             if (a.slopes && real) slope2 = a.slopes[h] * kLog2e;
@@ -555,8 +543,8 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         float m = -INFINITY;  // the row's reference, in step with the other group's
         float l = 0.f;        // this group's share of the row sum, relative to m
         uint64_t* my_dec = decided + grp * 4 + quarter;
-        uint64_t* their_dec = decided + (grp ^ 1) * 4 + quarter;
-        int slot = 0, turn = 0;  // i % kSlots, i / kSlots
+        // the group of the unit before this group's
+        uint64_t* their_dec = decided + (grp == 0 ? kGroups - 1 : grp - 1) * 4 + quarter;
         // The group's units in order, (n_blk, n_sub) without a division; what the
         // row sees of a unit is worked out one unit ahead.
         int n_blk = grp / upb, n_sub = grp % upb;
@@ -576,19 +564,21 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                 hi = min(win.hi - t0, kUnit - 1);
             }
             warp_any = __any_sync(0xffffffffu, hi >= lo);
-            n_sub += 2;
+            n_sub += kGroups;
             while (n_sub >= upb) {
                 n_sub -= upb;
                 ++n_blk;
             }
         };
         look(grp);
-        for (int i = 0; i < npairs; ++i) {
+        for (int u = grp, k = 0; u < 2 * npairs; u += kGroups, ++k) {
+            const int i = u >> 1, c = u & 1;               // the pair, the unit of it
+            const int slot = i % kSlots, turn = i / kSlots;
             const bool mine = hi >= lo;
-            const uint32_t scol = lane_addr + kColS + slot * 128 + grp * 64;
+            const uint32_t scol = lane_addr + kColS + slot * 128 + c * 64;
             if (!warp_any) {
                 // nothing of the unit concerns these rows: pass the references on, P = 0
-                if (grp == 1 || i > 0) tile_wait(their_dec, (grp == 1 ? i : i - 1) & 1, s_abort);
+                if (u > 0) tile_wait(their_dec, (grp == 0 ? k - 1 : k) & 1, s_abort);
                 if (lane == 0) mbar_arrive(my_dec);
                 tile_wait(&sfull[slot], turn & 1, s_abort);
                 tc_fence_after();
@@ -689,7 +679,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                 mx = mine ? mx * mul + lv : -INFINITY;
             }
             // the reference after the unit before this one, then after this one
-            if (grp == 1 || i > 0) tile_wait(their_dec, (grp == 1 ? i : i - 1) & 1, s_abort);
+            if (u > 0) tile_wait(their_dec, (grp == 0 ? k - 1 : k) & 1, s_abort);
             const float m_in = mref[r];
             float corr = 1.f;
             const bool moves = mx > m_in + kLazy;
@@ -735,7 +725,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
             if (any_moves && __any_sync(0xffffffffu, corr != 1.f)) {
                 // O holds earlier units of these rows: rescale once the previous
                 // unit's P V has landed
-                if (grp == 1)
+                if (c == 1)
                     tile_wait(&obar[slot], turn & 1, s_abort);
                 else
                     tile_wait(&vempty[(i - 1) & (kStages - 1)], ((i - 1) / kStages) & 1, s_abort);
@@ -758,39 +748,37 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                 tile_wait(&vfull[vs], (i / kStages) & 1, s_abort);
                 const int vr = r >> 1;
                 if (!there || t0 + vr >= ctx32) {
-                    unsigned char* vt = smem + kOffV + vs * kStageBytes + grp * kUnitBytes + vr * 128;
+                    unsigned char* vt = smem + kOffV + vs * kStageBytes + c * kUnitBytes + vr * 128;
 #pragma unroll
-                    for (int c = 4 * (r & 1); c < 4 * (r & 1) + 4; ++c)
-                        *reinterpret_cast<uint4*>(vt + ((c ^ (vr & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                    for (int x = 4 * (r & 1); x < 4 * (r & 1) + 4; ++x)
+                        *reinterpret_cast<uint4*>(vt + ((x ^ (vr & 7)) << 4)) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&pfull[2 * slot + grp]);
-            if (++slot == kSlots) {
-                slot = 0;
-                ++turn;
-            }
-            look(2 * (i + 1) + grp);
+            if (lane == 0) mbar_arrive(&pfull[2 * slot + c]);
+            look(u + kGroups);
         }
-        // ---------------- epilogue: O / l -> bf16, 64 dims per group ----------------
-        named_barrier_sync(kEndBarrier, kEndThreads);  // both groups' references are final
+        // ---------------- epilogue: O / l -> bf16, in chunks of 32 dims ----------------
+        named_barrier_sync(kEndBarrier, kEndThreads);  // every group's references are final
         const float m_end = mref[r];
         if (m_end != m) l *= fast_exp2(m - m_end);
         lsum[grp * 128 + r] = l;
         named_barrier_sync(kEndBarrier, kEndThreads);
         tile_wait(&drain[1], 0, s_abort);
         tc_fence_after();
-        const float L = *s_abort ? 0.f : lsum[r] + lsum[128 + r];
+        float L = 0.f;
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) L += lsum[k * 128 + r];
+        if (*s_abort) L = 0.f;
         const float inv = 1.f / L;
         if (a.lse && real && grp == 0) a.lse[qrow] = L == 0.f ? -INFINITY : m_end - kShift + log2f(L);
-        __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) + qrow * kHD + grp * 64;
+        __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) + qrow * kHD;
         bool bad = false;
-#pragma unroll
-        for (int ch = 0; ch < 2; ++ch) {
+        for (int ch = grp; ch < 4; ch += kGroups) {
             uint32_t ov[32];
-            tmem_ld32(lane_addr + kColO + grp * 64 + ch * 32, ov);
+            tmem_ld32(lane_addr + kColO + ch * 32, ov);
             if (real) {
                 uint32_t w[16];
 #pragma unroll
