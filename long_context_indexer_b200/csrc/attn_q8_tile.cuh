@@ -27,7 +27,8 @@
 // passes it by more than 3.75 (weights stay below 448), and O is rescaled only
 // then.
 //
-// Warps: 0 TMA producer, 1 issues Q K^T, 2 issues P V (the waits and commits
+// Warps: 0 copies K and 3 copies V (K runs ahead of the V ring, whose stages free
+// only after the softmax), 1 issues Q K^T, 2 issues P V (the waits and commits
 // around the one hide behind the MMAs of the other), then three softmax groups of
 // four warps that take every third unit, one thread per row. A warp (two queries
 // at 16 heads) none of whose queries selected the unit only stores zero weights,
@@ -63,7 +64,7 @@ constexpr int kMaxWords = 512;         // block bitmap words: nb_max <= 16384
 constexpr int kMaxUnion = 2048;        // distinct blocks per tile
 constexpr int kGroups = 3;             // softmax groups, unit u belongs to group u % kGroups
 constexpr int kGroupWarps = 4;
-constexpr int kFirstSoftmax = 3;       // warps 0..2: TMA, Q K^T, P V
+constexpr int kFirstSoftmax = 4;       // warps 0..3: K copies, Q K^T, P V, V copies
 constexpr int kThreads = 32 * kFirstSoftmax + kGroups * 32 * kGroupWarps;
 constexpr int kSlots = 3;              // pairs of S in flight
 // TMEM columns: O fp32, kSlots pairs of S (fp32; a unit's 64 columns then hold
@@ -417,45 +418,40 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
     // named barrier: the softmax warps before the epilogue
     constexpr int kEndBarrier = 1, kEndThreads = 32 * kGroups * kGroupWarps;
 
-    int issued = 0;  // pairs whose copies the producer thread started
-    if (warp == 0) {
-        // ---------------- TMA producer ----------------
+    int issued = 0;  // pairs whose copies this producer thread started
+    if (warp == 0 || warp == 3) {
+        // ---------------- TMA producers: K (warp 0) and V (warp 3) ----------------
         if (lane == 0) {
+            uint64_t* fullb = warp == 0 ? kfull : vfull;
+            uint64_t* emptyb = warp == 0 ? kempty : vempty;
+            const CUtensorMap* tm = warp == 0 ? &tm_k : &tm_v;
+            unsigned char* ring = smem + (warp == 0 ? kOffK : kOffV);
+            int blk = 0, sub = 0;
             for (int i = 0; i < npairs; ++i) {
-                const int st = i % kStages;
-                const uint32_t ph = ((i / kStages) - 1) & 1;
+                const int st = i & (kStages - 1);
                 int ys[2], nload = 0;
+#pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int u = 2 * i + c;
-                    ys[c] = -1;
-                    if (u < nunits) {
-                        const int blk = u / upb, sub = u - blk * upb;
-                        const int page = upage[blk];
-                        if (page >= 0) {
-                            ys[c] = (page * a.H_kv + g) * a.bs + sub * kUnit;
-                            ++nload;
-                        }
+                    const int page = 2 * i + c < nunits ? upage[blk] : -1;
+                    ys[c] = page >= 0 ? (page * a.H_kv + g) * a.bs + sub * kUnit : -1;
+                    nload += page >= 0 ? 1 : 0;
+                    if (++sub == upb) {
+                        sub = 0;
+                        ++blk;
                     }
                 }
-                bool ok = true;
+                if (i >= kStages) tile_wait(&emptyb[st], ((i / kStages) - 1) & 1, s_abort);
+                if (*s_abort) break;
                 issued = i + 1;
-                for (int kv = 0; kv < 2 && ok; ++kv) {
-                    uint64_t* full = kv ? &vfull[st] : &kfull[st];
-                    if (i >= kStages) tile_wait(kv ? &vempty[st] : &kempty[st], ph, s_abort);
-                    if (*s_abort) {
-                        ok = false;
-                        break;
-                    }
-                    unsigned char* dst = smem + (kv ? kOffV : kOffK) + st * kStageBytes;
-                    if (nload) {
-                        mbar_arrive_expect_tx(full, (uint32_t)nload * kUnitBytes);
-                        for (int c = 0; c < 2; ++c)
-                            if (ys[c] >= 0) tma_load_2d(dst + c * kUnitBytes, kv ? &tm_v : &tm_k, 0, ys[c], full);
-                    } else {
-                        mbar_arrive(full);
-                    }
+                if (nload) {
+                    mbar_arrive_expect_tx(&fullb[st], (uint32_t)nload * kUnitBytes);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        if (ys[c] >= 0)
+                            tma_load_2d(ring + st * kStageBytes + c * kUnitBytes, tm, 0, ys[c], &fullb[st]);
+                } else {
+                    mbar_arrive(&fullb[st]);
                 }
-                if (!ok) break;
             }
         }
     } else if (warp == 1) {
@@ -805,11 +801,9 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                      : "memory");
     }
     // a tile that gave up: its copies still land before the CTA's memory is reused
-    if (*s_abort && tid == 0)
-        for (int i = max(0, issued - kStages); i < issued; ++i) {
-            mbar_wait(&kfull[i % kStages], (i / kStages) & 1);
-            mbar_wait(&vfull[i % kStages], (i / kStages) & 1);
-        }
+    if (*s_abort && lane == 0 && (warp == 0 || warp == 3))
+        for (int i = max(0, issued - kStages); i < issued; ++i)
+            mbar_wait(&(warp == 0 ? kfull : vfull)[i & (kStages - 1)], (i / kStages) & 1);
     // rows that met a NaN (the K ring is free: every copy was consumed)
     if (!*s_abort)
         for (int r = warp; r < QT * G; r += kThreads / 32)
