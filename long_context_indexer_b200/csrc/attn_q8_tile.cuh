@@ -272,52 +272,149 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
     }
-    // ---------------- the union of the tile's selected blocks ----------------
-    // A thread's first entry is looked up (id, page, scales) while the union is
-    // counted, so the chain of global loads runs beside the barriers.
-    const int nent = QT * a.topk;
-    const int32_t* tile_ids = a.ids + ((size_t)b * a.S + s0) * a.topk;
-    const int n_real = min(QT, a.S - s0) * a.topk;  // entries of queries that exist
-    const int j_mine = tid < n_real ? __ldg(tile_ids + tid) : -1;
-    for (int w = tid; w < nwords; w += kThreads) bitmap[w] = 0u;
-    for (int e = tid; e < min(nent, kMaxUnion); e += kThreads) uinfo[e].y = 0u;
-    if (tid < kMaxQT) {
-        Q8Window w{0, -1, 0};
-        if (tid < QT && s0 + tid < a.S) w = q8_window(a, b * a.S + s0 + tid, b, s0 + tid);
-        wins[tid] = w;
-    }
-    if (tid < kRows) {
-        mref[tid] = -INFINITY;
-        redo[tid] = 0;
-    }
-    __syncthreads();
-    // ---- query rows -> shared memory, a warp per row (coalesced), beside the
-    // union: scaled so that the largest element is in [2^7, 2^8), high and low parts ----
-    if (warp >= kFirstSoftmax) {
+    constexpr int kUnionBarrier = 2, kUnionThreads = 32 * kFirstSoftmax;
+    if (warp < kFirstSoftmax) {
+        // ---------------- the union of the tile's selected blocks ----------------
+        // (warps 0..3, beside the query rows of the others)
+        constexpr int kHold = 4;  // entries, then blocks, a thread has in flight
+        const int32_t* tile_ids = a.ids + ((size_t)b * a.S + s0) * a.topk;
+        const int n_real = min(QT, a.S - s0) * a.topk;  // entries of queries that exist
+        int held[kHold];
+#pragma unroll
+        for (int k = 0; k < kHold; ++k) {
+            const int e = tid + k * kUnionThreads;
+            held[k] = e < n_real ? tile_ids[e] : -1;
+        }
+        for (int w = tid; w < nwords; w += kUnionThreads) bitmap[w] = 0u;
+        for (int e = tid; e < min(n_real, kMaxUnion); e += kUnionThreads) uinfo[e].y = 0u;
+        if (tid < kMaxQT) {
+            Q8Window w{0, -1, 0};
+            if (tid < QT && s0 + tid < a.S) w = q8_window(a, b * a.S + s0 + tid, b, s0 + tid);
+            wins[tid] = w;
+        }
+        named_barrier_sync(kUnionBarrier, kUnionThreads);
+        // block of entry e, the k-th of this thread, if its query can attend a
+        // token of it, else -1
+        auto entry = [&](int e, int k, int qi) -> int {
+            int j = -1;
+            if (k < kHold) {
+#pragma unroll
+                for (int x = 0; x < kHold; ++x) j = x == k ? held[x] : j;
+            } else {
+                j = tile_ids[e];
+            }
+            if (j < 0 || j >= a.nb_max) {
+                if (j != -1) raise_status(kStatusBadBlockId);
+                return -1;
+            }
+            const int first = j * a.bs;
+            return first <= wins[qi].hi && first + a.bs > wins[qi].lo ? j : -1;
+        };
+        for (int e = tid, k = 0; e < n_real; e += kUnionThreads, ++k) {
+            const int j = entry(e, k, e / a.topk);
+            if (j >= 0) atomicOr(&bitmap[j >> 5], 1u << (j & 31));
+        }
+        named_barrier_sync(kUnionBarrier, kUnionThreads);
+        if (warp == 0) {  // exclusive prefix of the words' population counts
+            const int per = (nwords + 31) / 32;
+            int sum = 0;
+            for (int k = 0; k < per; ++k) {
+                const int w = lane * per + k;
+                if (w < nwords) sum += __popc(bitmap[w]);
+            }
+            int incl = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int t = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += t;
+            }
+            int run = incl - sum;
+            for (int k = 0; k < per; ++k) {
+                const int w = lane * per + k;
+                if (w < nwords) {
+                    wpre[w] = (uint32_t)run;
+                    run += __popc(bitmap[w]);
+                }
+            }
+            if (lane == 31) *s_nunion = incl;
+        }
+        named_barrier_sync(kUnionBarrier, kUnionThreads);
+        for (int e = tid, k = 0; e < n_real; e += kUnionThreads, ++k) {
+            const int qi = e / a.topk;
+            const int j = entry(e, k, qi);
+            if (j >= 0) {
+                const int pos = (int)wpre[j >> 5] + __popc(bitmap[j >> 5] & ((1u << (j & 31)) - 1u));
+                uinfo[pos].x = (uint32_t)(j * a.bs);  // the same from every query that selected it
+                upage[pos] = j;
+                atomicOr(&uinfo[pos].y, 1u << qi);
+            }
+        }
+        named_barrier_sync(kUnionBarrier, kUnionThreads);
+        // the blocks' pages, then their scales, several in flight
+        const int n = *s_nunion;
+        for (int u0 = tid; u0 < n; u0 += kHold * kUnionThreads) {
+            int page[kHold];
+            float ks[kHold], vs[kHold];
+#pragma unroll
+            for (int k = 0; k < kHold; ++k) {
+                const int u = u0 + k * kUnionThreads;
+                page[k] = u < n ? a.table[(size_t)b * a.nb_max + upage[u]] : 0;
+            }
+#pragma unroll
+            for (int k = 0; k < kHold; ++k) {
+                const bool fine = page[k] >= 0 && page[k] < a.num_pages;
+                const size_t cell = fine ? (size_t)page[k] * a.H_kv + g : 0;
+                ks[k] = a.ks[cell];
+                vs[k] = a.vs[cell];
+                if (!fine) {
+                    raise_status(kStatusBadPage);
+                    page[k] = -1;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kHold; ++k) {
+                const int u = u0 + k * kUnionThreads;
+                if (u < n) {
+                    upage[u] = page[k];
+                    if (page[k] < 0) uinfo[u].x = ~0u;
+                    uinfo[u].z = __float_as_uint(ks[k]);
+                    uinfo[u].w = __float_as_uint(log2f(fmaxf(vs[k], kMinVScale)));
+                }
+            }
+        }
+    } else {
+        // ---- query rows -> shared memory, a warp per row (coalesced): scaled so
+        // that the largest element is in [2^7, 2^8), high and low parts ----
         constexpr int kQWarps = kGroups * kGroupWarps, kQRows = (kRows + kQWarps - 1) / kQWarps;
         const int w0 = warp - kFirstSoftmax;
+        const uint32_t inv_g = (65536u + G - 1) / G;  // r / G = r * inv_g >> 16 for r < 128, G <= 16
+        const __nv_bfloat16* q0 = static_cast<const __nv_bfloat16*>(a.q) +
+                                  (((size_t)b * a.S + s0) * a.H_q + (size_t)g * G) * kHD + 4 * lane;
         uint2 q4[kQRows];
 #pragma unroll
         for (int k = 0; k < kQRows; ++k) {
-            const int r = w0 + k * kQWarps, qi = r / G;
-            const bool real = r < QT * G && s0 + qi < a.S;
-            const size_t at = (((size_t)b * a.S + s0 + qi) * a.H_q + (size_t)g * G + (r - qi * G)) * kHD + 4 * lane;
-            q4[k] = real ? __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) + at))
+            const int r = w0 + k * kQWarps, qi = (int)((r * inv_g) >> 16);
+            const bool real = qi < QT && s0 + qi < a.S;
+            q4[k] = real ? *reinterpret_cast<const uint2*>(q0 + ((size_t)qi * a.H_q + (r - qi * G)) * kHD)
                          : make_uint2(0u, 0u);
         }
+        if (tid - kUnionThreads < kRows) mref[tid - kUnionThreads] = -INFINITY;
 #pragma unroll
         for (int k = 0; k < kQRows; ++k) {
             const int r = w0 + k * kQWarps;
             if (r >= kRows) break;
             float2 f0 = bf16x2_to_f32(q4[k].x), f1 = bf16x2_to_f32(q4[k].y);
-            const float amax = warp_max(fmaxf(fmaxf(fabsf(f0.x), fabsf(f0.y)), fmaxf(fabsf(f1.x), fabsf(f1.y))));
-            // a row with an infinity or a NaN is computed apart
-            const float sum = f0.x + f0.y + f1.x + f1.y;
-            if (__any_sync(0xffffffffu, !(fabsf(sum) <= 3.402823466e38f)) && lane == 0) redo[r] = 1;
-            int e = (int)(__float_as_uint(amax) >> 23) - 127;
+            // magnitudes order as their bits; infinities and NaN come out above
+            uint32_t top = max(max(__float_as_uint(fabsf(f0.x)), __float_as_uint(fabsf(f0.y))),
+                               max(__float_as_uint(fabsf(f1.x)), __float_as_uint(fabsf(f1.y))));
+            top = __reduce_max_sync(0xffffffffu, top);
+            int e = (int)(top >> 23) - 127;
             e = e < -100 ? -100 : e > 127 ? 127 : e;
             const float up = __uint_as_float((uint32_t)(7 - e + 127) << 23);
-            if (lane == 0) rowmul[r] = __uint_as_float((uint32_t)(e - 7 + 127) << 23);
+            if (lane == 0) {
+                rowmul[r] = __uint_as_float((uint32_t)(e - 7 + 127) << 23);
+                redo[r] = top >= 0x7f800000u ? 1 : 0;  // such a row is computed apart
+            }
             f0.x *= up;
             f0.y *= up;
             f1.x *= up;
@@ -333,87 +430,14 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         }
         fence_proxy_async_smem();
     }
-    // block of entry e if its query can attend a token of it, else -1
-    auto entry = [&](int e, int qi) -> int {
-        const int j = e == tid ? j_mine : __ldg(tile_ids + e);
-        if (j < 0 || j >= a.nb_max) {
-            if (j != -1) raise_status(kStatusBadBlockId);
-            return -1;
-        }
-        const int first = j * a.bs;
-        return first <= wins[qi].hi && first + a.bs > wins[qi].lo ? j : -1;
-    };
-    auto lookup = [&](int j, int& page, float& ks, float& vs) {
-        page = __ldg(a.table + (size_t)b * a.nb_max + j);
-        if (page < 0 || page >= a.num_pages) {
-            raise_status(kStatusBadPage);
-            page = -1;
-            ks = vs = 0.f;
-        } else {
-            const size_t cell = (size_t)page * a.H_kv + g;
-            ks = __ldg(a.ks + cell);
-            vs = __ldg(a.vs + cell);
-        }
-    };
-    int page_mine = -1;
-    float ks_mine = 0.f, vs_mine = 0.f;
-    for (int e = tid; e < n_real; e += kThreads) {
-        const int j = entry(e, e / a.topk);
-        if (j >= 0) {
-            atomicOr(&bitmap[j >> 5], 1u << (j & 31));
-            if (e == tid) lookup(j, page_mine, ks_mine, vs_mine);
-        }
-    }
-    __syncthreads();
-    if (warp == 0) {  // exclusive prefix of the words' population counts
-        const int per = (nwords + 31) / 32;
-        int sum = 0;
-        for (int k = 0; k < per; ++k) {
-            const int w = lane * per + k;
-            if (w < nwords) sum += __popc(bitmap[w]);
-        }
-        int incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int t = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += t;
-        }
-        int run = incl - sum;
-        for (int k = 0; k < per; ++k) {
-            const int w = lane * per + k;
-            if (w < nwords) {
-                wpre[w] = (uint32_t)run;
-                run += __popc(bitmap[w]);
-            }
-        }
-        if (lane == 31) *s_nunion = incl;
-    }
-    __syncthreads();
-    for (int e = tid; e < n_real; e += kThreads) {
-        const int qi = e / a.topk;
-        const int j = entry(e, qi);
-        if (j >= 0) {
-            const int pos = (int)wpre[j >> 5] + __popc(bitmap[j >> 5] & ((1u << (j & 31)) - 1u));
-            int page = page_mine;
-            float ks = ks_mine, vs = vs_mine;
-            if (e != tid) lookup(j, page, ks, vs);
-            // every query that selected the block writes the same values
-            uinfo[pos].x = page >= 0 ? (uint32_t)(j * a.bs) : ~0u;
-            uinfo[pos].z = __float_as_uint(ks);
-            uinfo[pos].w = __float_as_uint(log2f(fmaxf(vs, kMinVScale)));
-            upage[pos] = page;
-            atomicOr(&uinfo[pos].y, 1u << qi);
-        }
-    }
-    __syncthreads();
-    const int nunion = *s_nunion;
-    const int nunits = nunion * upb;
-    const int npairs = (nunits + 1) / 2;
     const long long ctx = a.ctx_len[b];
 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    const int nunion = *s_nunion;
+    const int nunits = nunion * upb;
+    const int npairs = (nunits + 1) / 2;
     const uint32_t tmem_base = *tmem_slot;
     // named barrier: the softmax warps before the epilogue
     constexpr int kEndBarrier = 1, kEndThreads = 32 * kGroups * kGroupWarps;
@@ -770,27 +794,47 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         if (*s_abort) L = 0.f;
         const float inv = 1.f / L;
         if (a.lse && real && grp == 0) a.lse[qrow] = L == 0.f ? -INFINITY : m_end - kShift + log2f(L);
-        __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(a.out) + qrow * kHD;
+        // through the K ring (every copy and MMA of it is done), rows padded by 16
+        // bytes, so that rows leave whole
+        constexpr int kPitch = 2 * kHD + 16;
         bool bad = false;
         for (int ch = grp; ch < 4; ch += kGroups) {
             uint32_t ov[32];
             tmem_ld32(lane_addr + kColO + ch * 32, ov);
-            if (real) {
-                uint32_t w[16];
+            uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    // a row that attends nothing is zero whatever O holds
-                    const float x = L == 0.f ? 0.f : __uint_as_float(ov[2 * e]) * inv;
-                    const float y = L == 0.f ? 0.f : __uint_as_float(ov[2 * e + 1]) * inv;
-                    bad = bad || x != x || y != y;
-                    w[e] = pack_bf16x2(x, y);
-                }
-                uint4* dst = reinterpret_cast<uint4*>(orow + ch * 32);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            for (int e = 0; e < 16; ++e) {
+                // a row that attends nothing is zero whatever O holds
+                const float x = L == 0.f ? 0.f : __uint_as_float(ov[2 * e]) * inv;
+                const float y = L == 0.f ? 0.f : __uint_as_float(ov[2 * e + 1]) * inv;
+                bad = bad || x != x || y != y;
+                w[e] = pack_bf16x2(x, y);
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<uint4*>(smem + kOffK + r * kPitch + ch * 64 + 16 * e) =
+                    make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
         }
-        if (bad) redo[r] = 1;
+        if (real && bad) redo[r] = 1;
+        named_barrier_sync(kEndBarrier, kEndThreads);
+        const uint32_t inv_g = (65536u + G - 1) / G;
+        __nv_bfloat16* o0 = static_cast<__nv_bfloat16*>(a.out) + (((size_t)b * a.S + s0) * a.H_q + (size_t)g * G) * kHD;
+        for (int x = tid - 32 * kFirstSoftmax; x < kRows * 16; x += kEndThreads) {
+            const int row = x >> 4, c = x & 15, q = (int)((row * inv_g) >> 16);
+            if (q < QT && s0 + q < a.S)
+                *reinterpret_cast<uint4*>(o0 + ((size_t)q * a.H_q + (row - q * G)) * kHD + 8 * c) =
+                    *reinterpret_cast<const uint4*>(smem + kOffK + row * kPitch + 16 * c);
+        }
+        // rows that met a NaN, a warp each
+        const bool again = __any_sync(0xffffffffu, redo[lane] | redo[lane + 32] | redo[lane + 64] | redo[lane + 96]);
+        if (again) {
+            named_barrier_sync(kEndBarrier, kEndThreads);  // all rows have left the K ring
+            if (!*s_abort)
+                for (int x = warp - kFirstSoftmax; x < QT * G; x += kGroups * kGroupWarps)
+                    if (redo[x] && s0 + x / G < a.S)
+                        q8_row_by_warp(a, b * a.S + s0 + x / G, g * G + x % G,
+                                       reinterpret_cast<float*>(smem + kOffK) + warp * kHD);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -804,12 +848,6 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
     if (*s_abort && lane == 0 && (warp == 0 || warp == 3))
         for (int i = max(0, issued - kStages); i < issued; ++i)
             mbar_wait(&(warp == 0 ? kfull : vfull)[i & (kStages - 1)], (i / kStages) & 1);
-    // rows that met a NaN (the K ring is free: every copy was consumed)
-    if (!*s_abort)
-        for (int r = warp; r < QT * G; r += kThreads / 32)
-            if (redo[r] && s0 + r / G < a.S)
-                q8_row_by_warp(a, b * a.S + s0 + r / G, g * G + r % G,
-                               reinterpret_cast<float*>(smem + kOffK) + warp * kHD);
 }
 
 }  // namespace lci
