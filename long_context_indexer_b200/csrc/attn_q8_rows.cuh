@@ -220,8 +220,10 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
     int n_blk = -1, n_x = 0, st = 0, st_end = 0, n_t0 = 0;
     const uint8_t *kp = nullptr, *vp = nullptr;
     // A warp with few strips asks L2 for all of them at once: one round trip to
-    // HBM (and to the page tables of a large pool) instead of one per strip.
-    const bool few = w1 - w0 <= kPrefetch;
+    // HBM (and to the page tables of a large pool) instead of one per strip. Not
+    // where queries of one sequence share blocks: they would ask for them often
+    // (89 queries of 11 blocks: 37 us).
+    const bool few = w1 - w0 <= kPrefetch && a.S == 1;
     auto lookup = [&](int j) {
         t_lane = -1;
         const int page = q8_page(a, b, j, win);

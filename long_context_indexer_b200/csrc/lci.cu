@@ -1633,15 +1633,29 @@ lci_status launch_tile(const lci::AttnQ8Args& a, int32_t batch, const lci_block_
     return check_launch("sparse_attn_q8");
 }
 
-// Which schedule a call takes: the tile schedule when asked for and it fits,
-// or, left to choose, for many queries per sequence whose selections are likely
-// to share blocks (at most four times as many blocks as a tile's queries select
-// in all); otherwise the row-wise one.
+// Which schedule a call takes: the tile schedule when asked for and it fits, or,
+// left to choose, the one with the lower estimate, in SM cycles. A tile costs
+// about 16 K of set-up and output and 1030 per 64-token unit of its union (1700
+// when scores are capped or biased), a row 2800 and 800 (1000) per unit, the
+// row-wise launch 8 K; the union is that of random selections. Measured, tile
+// against rows: 11 blocks, 888 queries of 4 heads 25 us / 74; 3 blocks, 264 rows
+// 15.7 / 9.9; 116 blocks, 5 of them for each of 1880 rows 38 / 50; 288 blocks, 9 for
+// each of 5838 rows with a cap 304 / 224.
 bool use_tile_q8(const lci::AttnQ8Args& a, lci_dtype dtype, const lci_block_table* t,
-                 lci_phase phase) {
+                 int32_t batch, lci_phase phase) {
     if (phase == LCI_PHASE_DECODE || !tile_q8_fits(a, dtype, t)) return false;
     if (phase == LCI_PHASE_PREFILL) return true;
-    return a.S >= 16 && (long long)a.nb_max <= 4ll * tile_q8_queries(a) * a.topk;
+    if (a.S == 1) return false;
+    constexpr double kSMs = 148;
+    const bool mods = a.cap > 0.f || a.slopes;
+    const int QT = tile_q8_queries(a);
+    const double nb = a.nb_max, k = std::min(a.topk, a.nb_max), upb = a.bs / lci::q8t::kUnit;
+    const double queries = std::min(QT, a.S);
+    const double uni = nb * (1.0 - std::pow(1.0 - k / nb, queries));
+    const double tiles = (double)batch * a.H_kv * ((a.S + QT - 1) / QT);
+    const double tile = std::ceil(tiles / kSMs) * (16e3 + uni * upb * (mods ? 1700 : 1030));
+    const double rows = 8e3 + (double)batch * a.H_kv * a.S * (2800 + k * upb * (mods ? 1000 : 800)) / kSMs;
+    return tile < rows;
 }
 
 template <int IPT>
@@ -1759,7 +1773,7 @@ lci_status lci_sparse_attn_q8(const void* q, lci_dtype dtype, int32_t batch, int
     a.mass = d_mass;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const bool mods = a.cap > 0.f || a.slopes;
-    if (use_tile_q8(a, dtype, table, phase))
+    if (use_tile_q8(a, dtype, table, batch, phase))
         return mods ? launch_tile<true>(a, batch, table, cs) : launch_tile<false>(a, batch, table, cs);
     const long long pairs = (long long)batch * S * a.H_kv;
     if (rows_q8_fits(a, dtype) && pairs < (1ll << 27)) {
