@@ -165,14 +165,22 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
     const int G = a.H_q / a.H_kv;
     const int b = row / a.S, s = row - b * a.S;
     const int spb = a.bs / kStrip;  // strips per block
+
+    pdl_wait();  // nothing of global memory is read before
+    // Entries up to the last block: the -1 entries behind it (fewer visible blocks
+    // than topk) take no part in the split.
+    const int32_t* all_ids = a.ids + (size_t)row * a.topk;
+    const int id_a = lane < a.topk ? all_ids[lane] : -1, id_b = lane + 32 < a.topk ? all_ids[lane + 32] : -1;
+    int n_ent = id_b != -1 ? lane + 33 : id_a != -1 ? lane + 1 : 0;
+    for (int i = lane + 64; i < a.topk; i += 32)
+        if (all_ids[i] != -1) n_ent = i + 1;
+    n_ent = (int)__reduce_max_sync(0xffffffffu, (unsigned)n_ent);
     // this CTA's blocks, this warp's strips of them
-    const int per = (a.topk + nsplit - 1) / nsplit;
-    const int i0 = min(a.topk, split * per), nblk = min(a.topk, i0 + per) - i0;
+    const int per = (n_ent + nsplit - 1) / nsplit;
+    const int i0 = min(n_ent, split * per), nblk = min(n_ent, i0 + per) - i0;
     const int nstrips = nblk * spb;
     const int wper = (nstrips + NW - 1) / NW;
     const int w0 = min(nstrips, warp * wper), w1 = min(nstrips, w0 + wper);
-
-    pdl_wait();  // nothing of global memory is read before
     if (nsplit > 1) cluster_arrive_relaxed();  // matched before the first remote store
     const bool mass = a.mass != nullptr;
     if (mass) {
@@ -183,10 +191,13 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
 
     // The loads that depend on nothing go first, all in flight together: the
     // ids of this warp's first 32 blocks, the query rows, the positions.
-    const int32_t* row_ids = a.ids + (size_t)row * a.topk + i0;
+    const int32_t* row_ids = all_ids + i0;
     const int blk_end = w1 > w0 ? (w1 - 1) / spb + 1 : 0;
     int base = w1 > w0 ? w0 / spb : 0;  // blocks are looked up 32 at a time, one per lane
-    const int j_first = base + lane < blk_end ? row_ids[base + lane] : -1;
+    // (of the first 64 entries the ids are at hand)
+    const int at = i0 + base + lane;
+    const int ja = __shfl_sync(0xffffffffu, id_a, at & 31), jb = __shfl_sync(0xffffffffu, id_b, at & 31);
+    const int j_first = base + lane < blk_end ? (at < 32 ? ja : at < 64 ? jb : all_ids[at]) : -1;
     uint4 qraw[2][HD / 64][2];
     {
         const __nv_bfloat16* qrow = static_cast<const __nv_bfloat16*>(a.q) + ((size_t)row * a.H_q + (size_t)g * G) * HD;
@@ -592,6 +603,8 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
         // mass of block i: over the warps that met it and the group's heads,
         // four lanes sharing a block's heads
         float* mrow = a.mass + ((size_t)row * a.H_kv + g) * a.topk + i0;
+        if (split == nsplit - 1)
+            for (int i = n_ent - i0 + tid; i < a.topk - i0; i += NT) mrow[i] = 0.f;
         for (int e = tid; e < nblk * 4; e += NT) {
             const int i = e >> 2, part = e & 3;
             const uint32_t quad = 0xfu << (lane & 28);
