@@ -52,7 +52,7 @@ template <int HD, int NW> __host__ __device__ constexpr int o_floats() { return 
 template <int HD, int NW> __host__ __device__ constexpr int base_floats() {
     return o_floats<HD, NW>() + NW * kRows * 2 /*warps' max, sum*/ +
            kRows * HD + 4 * kMaxSplit /*slices received*/ +
-           kMaxSplit * kRows * 2 /*CTAs' max, sum*/;
+           kMaxSplit * kRows * 2 /*CTAs' max, sum*/ + HD * 8 /*query fragments*/;
 }
 // (max, sum) per head of each (block, warp) that meet: blocks + warps entries
 template <int HD, int NW>
@@ -119,12 +119,14 @@ template <int HD>
 struct Q8Strip {
     uint4 k[2][HD / 64];        // [8-token half][16-byte run]
     uint32_t v[4][HD / 32];     // [token 2q, 2q+1, 2q+8, 2q+9][words]
-    __device__ __forceinline__ void load(const uint8_t* kp, const uint8_t* vp, int g8, int q4) {
+    __device__ __forceinline__ void load_k(const uint8_t* kp, int g8, int q4) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int c = 0; c < HD / 64; ++c)
                 k[j][c] = __ldg(reinterpret_cast<const uint4*>(kp + (8 * j + g8) * HD + 16 * (q4 + 4 * c)));
+    }
+    __device__ __forceinline__ void load_v(const uint8_t* vp, int g8, int q4) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const uint8_t* p = vp + (2 * q4 + (t & 1) + 8 * (t >> 1)) * HD + g8 * (HD / 8);
@@ -143,8 +145,15 @@ struct Q8Strip {
     }
 };
 
-template <int HD, int NW, bool MODS>
-__global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_kernel(
+// kLean: three CTAs of four warps per SM, for many rows. The query's fragments
+// come from shared memory and a strip's registers take the next strip as soon as
+// they are read (its K during this one's softmax and P V, its V during the next Q
+// K^T); with more warps to hide the loads this gives 15-25 % (320 pairs of 21
+// blocks: 29 us against 38). Else queries and a whole further strip are held in
+// registers, which shortens the chain of a few rows (32 x 32 blocks: 9.4 us against
+// 9.8).
+template <int HD, int NW, bool MODS, bool kLean>
+__global__ void __launch_bounds__(NW * 32, kLean ? 3 : NW == 4 ? 2 : 1) sparse_attn_q8_rows_kernel(
     const __grid_constant__ AttnQ8Args a, int nsplit) {
     using namespace q8r;
     namespace cg = cooperative_groups;
@@ -156,7 +165,8 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
     float* sml = so + o_floats<HD, NW>();                 // [NW][16][max, sum]
     float* recv = sml + NW * kRows * 2;                   // this CTA's slice, from each CTA
     float* cml = recv + kRows * HD + 4 * kMaxSplit;       // [CTA][16][max, sum]
-    float* sbm = cml + kMaxSplit * kRows * 2;             // [block + warp][16][max, sum]
+    uint4* sq = reinterpret_cast<uint4*>(cml + kMaxSplit * kRows * 2);  // [k-step][lane]
+    float* sbm = cml + kMaxSplit * kRows * 2 + HD * 8;    // [block + warp][16][max, sum]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g8 = lane >> 2, q4 = lane & 3;
     const int split = blockIdx.x % nsplit;
@@ -279,11 +289,14 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
     Q8Strip<HD> cur, nxt;
     lookup(j_first);
     bool have = blk_end > 0 && advance();
-    if (have) cur.load(kp + (size_t)st * kStrip * HD, vp + (size_t)st * kStrip * HD, g8, q4);
+    if (have) {
+        cur.load_k(kp + (size_t)st * kStrip * HD, g8, q4);
+        cur.load_v(vp + (size_t)st * kStrip * HD, g8, q4);
+    }
 
     // the group's query rows, scaled to f16 (head rows g8 and g8 + 8)
-    uint32_t qf[KS][4];
     float qs_a, qs_b;  // what a row's logits are multiplied by (with the softmax scale)
+    uint32_t qf[KS][4];
     {
         float back[2];
 #pragma unroll
@@ -323,6 +336,13 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
         const float unit = MODS ? a.scale : a.scale * kLog2e;
         qs_a = unit * back[0];
         qs_b = unit * back[1];
+        if constexpr (kLean) {
+            // the same for every warp: each leaves its share of the k-steps for all
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+                if (k % NW == warp) sq[k * 32 + lane] = make_uint4(qf[k][0], qf[k][1], qf[k][2], qf[k][3]);
+            __syncthreads();
+        }
     }
     float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;  // l: this lane's share
     float r_a = 0.f, r_b = 0.f;                                    // the current block's share
@@ -353,8 +373,14 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
         // a block's scales stay with the lane that looked it up until now
         const float c_ks = __shfl_sync(0xffffffffu, ks_lane, n_x);
         const VScale c_vs = split_v_scale(__shfl_sync(0xffffffffu, vs_lane, n_x));
-        const bool more = advance();
-        if (more) nxt.load(kp + (size_t)st * kStrip * HD, vp + (size_t)st * kStrip * HD, g8, q4);
+        bool more = false;
+        if constexpr (!kLean) {
+            more = advance();
+            if (more) {
+                nxt.load_k(kp + (size_t)st * kStrip * HD, g8, q4);
+                nxt.load_v(vp + (size_t)st * kStrip * HD, g8, q4);
+            }
+        }
 
         // S = Q K^T: two n-tiles of 8 tokens
         // in two chains each (even and odd k-steps)
@@ -366,14 +392,27 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
 #pragma unroll
         for (int c = 0; c < HD / 64; ++c)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 4; ++k) {
+                uint32_t qk[4] = {qf[4 * c + k][0], qf[4 * c + k][1], qf[4 * c + k][2], qf[4 * c + k][3]};
+                if constexpr (kLean) {
+                    const uint4 w = sq[(4 * c + k) * 32 + lane];
+                    qk[0] = w.x;
+                    qk[1] = w.y;
+                    qk[2] = w.z;
+                    qk[3] = w.w;
+                }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const uint32_t w[4] = {cur.k[j][c].x, cur.k[j][c].y, cur.k[j][c].z, cur.k[j][c].w};
                     uint32_t b0, b1;
                     e4m3x4_to_f16(w[k], b0, b1);
-                    mma_f16_16816(k & 1 ? sd[j] : sc[j], qf[4 * c + k], b0, b1);
+                    mma_f16_16816(k & 1 ? sd[j] : sc[j], qk, b0, b1);
                 }
+            }
+        if constexpr (kLean) {
+            more = advance();
+            if (more) cur.load_k(kp + (size_t)st * kStrip * HD, g8, q4);
+        }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -493,9 +532,12 @@ __global__ void __launch_bounds__(NW * 32, NW == 4 ? 2 : 1) sparse_attn_q8_rows_
             mma_f16_16816(o[4 * w + 2], pf, x2, y2);
             mma_f16_16816(o[4 * w + 3], pf, x3, y3);
         }
+        if constexpr (kLean) {
+            if (more) cur.load_v(vp + (size_t)st * kStrip * HD, g8, q4);
+        }
         if (!more || n_blk != c_blk) close_block(c_blk);
         have = more;
-        cur = nxt;
+        if constexpr (!kLean) cur = nxt;
     }
 
     // ---- the warps' partials: (max, sum) and O in shared memory ----

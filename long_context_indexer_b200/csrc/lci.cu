@@ -1528,10 +1528,10 @@ struct KernelSetup {
 // 8 CTAs, at most one per block) whose clusters the device holds all at once; a
 // second wave costs more than longer runs per warp (16 pairs: 25.2 us with
 // clusters of 8, of which 16 do not fit, against 17.8 with clusters of 4).
-template <int HD, int NW, bool MODS>
+template <int HD, int NW, bool MODS, bool LEAN>
 struct Q8Rows {
     static KernelSetup setup;
-    static constexpr auto kern = lci::sparse_attn_q8_rows_kernel<HD, NW, MODS>;
+    static constexpr auto kern = lci::sparse_attn_q8_rows_kernel<HD, NW, MODS, LEAN>;
     static size_t smem(const lci::AttnQ8Args& a, int nsplit) {
         return lci::q8r::smem_bytes<HD, NW>(a.mass ? (a.topk + nsplit - 1) / nsplit : 0);
     }
@@ -1552,24 +1552,26 @@ struct Q8Rows {
         return check_launch("sparse_attn_q8");
     }
 };
-template <int HD, int NW, bool MODS> KernelSetup Q8Rows<HD, NW, MODS>::setup;
+template <int HD, int NW, bool MODS, bool LEAN> KernelSetup Q8Rows<HD, NW, MODS, LEAN>::setup;
 
 // Few pairs: eight warps per CTA, one CTA per SM, as many CTAs per pair as fit.
-// Else four warps per CTA, two CTAs per SM, each pair whole once they fill the
-// GPU.
+// Some more: four warps per CTA, two CTAs per SM. From the pairs that fill those on
+// (296), the lean form with three CTAs per SM, each pair whole.
 template <int HD, bool MODS>
 lci_status launch_rows(const lci::AttnQ8Args& a, long long pairs, cudaStream_t st) {
-    using Few = Q8Rows<HD, 8, MODS>;
-    using Many = Q8Rows<HD, 4, MODS>;
-    cudaError_t e = Few::prepare();
-    if (e == cudaSuccess) e = Many::prepare();
+    using Few = Q8Rows<HD, 8, MODS, false>;
+    using Some = Q8Rows<HD, 4, MODS, false>;
+    using Many = Q8Rows<HD, 4, MODS, true>;
+    cudaError_t e = pairs > 2 * 148 ? Many::prepare() : Some::prepare();
+    if (e == cudaSuccess && pairs <= 148) e = Few::prepare();
     if (e != cudaSuccess) return fail(LCI_ERR_CUDA, "sparse_attn_q8: %s", cudaGetErrorString(e));
+    if (pairs > 2 * 148) return Many::launch(a, pairs, 1, st);
+    const int some = Some::best_split(a, pairs);
     if (pairs <= 148) {
-        const int few = Few::best_split(a, pairs), many = Many::best_split(a, pairs);
-        if (2 * few >= many) return Few::launch(a, pairs, few, st);
-        return Many::launch(a, pairs, many, st);
+        const int few = Few::best_split(a, pairs);
+        if (2 * few >= some) return Few::launch(a, pairs, few, st);
     }
-    return Many::launch(a, pairs, pairs <= 2 * 148 ? Many::best_split(a, pairs) : 1, st);
+    return Some::launch(a, pairs, some, st);
 }
 
 // The tile schedule (attn_q8_tile.cuh).
