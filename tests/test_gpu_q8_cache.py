@@ -357,6 +357,99 @@ def test_other_streams_and_captured_calls_give_the_same():
     lci.get_device_status()
 
 
+WIDE = [  # tiles of many blocks, odd head groups, several KV heads, lists longer than what is visible
+    (torch.bfloat16, 1, 40, 38500, 1, 4, 128, 64, 64),
+    (torch.bfloat16, 1, 45, 900, 4, 3, 128, 64, 200),
+    (torch.bfloat16, 2, 19, 400, 1, 7, 128, 128, 5),
+    (torch.bfloat16, 1, 33, 330, 2, 1, 128, 64, 4),
+    (torch.bfloat16, 1, 9, 1030, 1, 13, 128, 192, 6),
+    (torch.bfloat16, 90, 4, 250, 1, 2, 128, 64, 5),
+    (torch.bfloat16, 40, 4, 250, 2, 8, 64, 16, 20),
+]
+
+
+@pytest.mark.parametrize("phase", ["prefill", "decode"])
+@pytest.mark.parametrize("shape", WIDE)
+def test_wide_unions_and_odd_groups(shape, phase):
+    check_attention(*attention_inputs(shape, 90), phase=phase, mass=phase != "prefill", p_bits=8 if phase == "prefill" else 11)
+
+
+def test_cells_past_four_gigabytes():
+    """Pools of 4.5 GB: the last pages' bytes lie past 32-bit offsets."""
+    H, bs, hd, P, n = 1, 128, 128, 275000, 300
+    cache = lci.Q8Cache(P, H, bs, hd, "cuda")
+    table = torch.tensor([[P - 1, 3, P - 2], [P - 3, P - 4, 5]], dtype=torch.int32)
+    bt = lci.create_block_table(table.cuda(), cache.k)
+    g = torch.Generator().manual_seed(2)
+    k_new, v_new = (torch.randn(2, n, H, hd, generator=g).to(torch.bfloat16) for _ in range(2))
+    start = torch.zeros(2, dtype=torch.int32)
+    lci.kv_append_q8(cache, bt, k_new.cuda(), v_new.cuda(), start.cuda())
+    pages = table.flatten().long()
+    small = [t[pages.cuda()].cpu() for t in (cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scale, cache.v_scale)]
+    local = torch.arange(6, dtype=torch.int32).reshape(2, 3)
+    want = ref.append(torch.zeros(6, H, bs, hd), torch.zeros(6, H, bs, hd), torch.ones(6, H), torch.ones(6, H), local, bs, k_new, v_new, start)
+    assert torch.equal(small[0].view(E4M3).float().double(), want[0]) and torch.equal(small[3].double(), want[3])
+    S = 24
+    q = torch.randn(2, S, 16, hd, generator=g).to(torch.bfloat16)
+    ids = random_ids(2, S, 3, 3, g, hole=0.0)
+    ctx = torch.tensor([n, n], dtype=torch.int32)
+    ro, _, _, sizes = ref.attend(q, want[0], want[1], want[2], want[3], local, bs, ids, ctx, ctx - S)
+    for phase, bits in (("prefill", 8), ("decode", 11)):
+        out = lci.sparse_attn_q8(q.cuda(), cache, bt, ids.cuda(), ctx.cuda(), (ctx - S).cuda(), phase=phase)
+        torch.cuda.synchronize()
+        lci.get_device_status()
+        assert ((out.cpu().double() - ro).abs() <= ref.out_tolerance(ro, sizes, q.dtype, hd, bits)).all()
+
+
+def test_calls_on_two_streams_at_once():
+    """Two caches, two tables, two streams, no shared state: each call's result is
+    what it is alone."""
+    made = []
+    for i, shape in enumerate((SHAPES[5], SHAPES[4], SHAPES[0])):
+        q, cache, table, cpu, bs, ids, ctx_len, q_start = attention_inputs(shape, 100 + i)
+        bt = lci.create_block_table(table.cuda(), cache.k)
+        call = lci.prepare_sparse_attn_q8(*(x.cuda() if isinstance(x, torch.Tensor) else x for x in (q, cache, bt, ids, ctx_len, q_start)), lse=True)
+        made.append((call, [t.clone() for t in call()]))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    for _ in range(20):
+        for st, (call, _) in zip(streams, made):
+            call(st)
+    torch.cuda.synchronize()
+    lci.get_device_status()
+    for call, want in made:
+        assert all(torch.equal(a, b) for a, b in zip(call.result, want))
+
+
+def test_refusals_of_the_binding():
+    q, cache, table, cpu, bs, ids, ctx_len, q_start = attention_inputs(SHAPES[0], 110)
+    bt = lci.create_block_table(table.cuda(), cache.k)
+    d = [t.cuda() for t in (q, ids, ctx_len, q_start)]
+    with pytest.raises(ValueError):  # not contiguous
+        lci.sparse_attn_q8(d[0].transpose(1, 2).contiguous().transpose(1, 2)[:, :, ::2], cache, bt, d[1], d[2], d[3])
+    with pytest.raises(TypeError):
+        lci.sparse_attn_q8(d[0].half(), cache, bt, d[1], d[2], d[3])
+    with pytest.raises(ValueError):
+        lci.sparse_attn_q8(d[0], cache, bt, d[1], d[2][:1], d[3])
+    with pytest.raises(ValueError):
+        lci.sparse_attn_q8(d[0], cache, bt, d[1], d[2], d[3], slopes=torch.ones(3, device="cuda"))
+    with pytest.raises(TypeError):
+        lci.sparse_attn_q8(d[0], cache, bt, d[1], d[2], d[3], first=torch.zeros(2, 1, device="cuda"))
+    with pytest.raises(ValueError):
+        lci.sparse_attn_q8(d[0], cache, bt, d[1], d[2], d[3].cpu())
+    with pytest.raises(ValueError):  # another cache's pools
+        lci.sparse_attn_q8(d[0], lci.Q8Cache(3, 1, 64, 128, "cuda"), bt, d[1], d[2], d[3])
+    with pytest.raises(TypeError):  # a table over bf16 pools
+        lci.kv_append_q8(cache, lci.create_block_table(table.cuda(), cache.k.to(torch.bfloat16)), torch.zeros(2, 1, 1, 128, device="cuda"),
+                         torch.zeros(2, 1, 1, 128, device="cuda"), d[2])
+    with pytest.raises(lci.LciError):
+        lci.cache_evict(bt, d[2], torch.zeros(table.shape, device="cuda"), 3, sink=2, recent=2)
+    with pytest.raises(lci.LciError):
+        lci.block_weight_update(torch.zeros(2, 5, device="cuda"), d[1], torch.zeros(2, 1, 1, 4, device="cuda"), decay=-1.0)
+    with pytest.raises(lci.LciError):  # the bf16 attention does not take this table
+        lci.sparse_attn_workspace_size(2, 1, 16, 4, bt)
+
+
 # ---------------------------------------------------------------- weights and eviction
 
 @pytest.mark.parametrize("B,S,H,topk,NB,decay", [(1, 1, 1, 1, 1, 1.0), (3, 1, 2, 8, 40, 0.5), (2, 70, 1, 32, 100, 1.0),
@@ -424,6 +517,47 @@ def test_eviction_of_special_weights_and_lengths():
     assert t[0].tolist() == [0, 2, 3, 6, 7, 1, 4, 5] and c.tolist() == [80, 0, 16, 129]
     assert t[3].tolist() == table[3].tolist() and w[3].tolist() == weight[3].tolist()
     assert kept[1].tolist() == [-1] * 5 and kept[2].tolist() == [0, -1, -1, -1, -1]
+
+
+def test_captured_serving_step_replays():
+    """Append, attention with masses and the weights' update as one graph, replayed
+    with new inputs in the same buffers, against the same calls made one by one."""
+    B, H, G, hd, bs, NB = 3, 2, 4, 128, 64, 5
+    g = torch.Generator().manual_seed(13)
+    table = make_table(B, NB, B * NB, g).cuda()
+    state = []
+    for _ in range(2):
+        cache = lci.Q8Cache(B * NB, H, bs, hd, "cuda")
+        state.append((cache, lci.create_block_table(table, cache.k), torch.zeros(B, NB, device="cuda")))
+    new = [torch.zeros(B, 1, H, hd, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    q = torch.zeros(B, 1, H * G, hd, dtype=torch.bfloat16, device="cuda")
+    pos = torch.full((B,), 70, dtype=torch.int32, device="cuda")
+    ctx = pos + 1
+    ids = torch.tensor([1, 0, -1], dtype=torch.int32, device="cuda").repeat(B, 1, 1)
+
+    def step(cache, bt, weight):
+        lci.kv_append_q8(cache, bt, new[0], new[1], pos)
+        out, mass = lci.sparse_attn_q8(q, cache, bt, ids, ctx, pos, mass=True)
+        lci.block_weight_update(weight, ids, mass, decay=0.5)
+        return out
+    prompt = [torch.randn(B, 70, H, hd, generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+    for cache, bt, _ in state:
+        lci.kv_append_q8(cache, bt, prompt[0], prompt[1], torch.zeros_like(pos))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out_g = step(*state[0])
+    for t in range(4):
+        for x in new + [q]:
+            x.copy_(torch.randn(x.shape, generator=g) * (1 + t))
+        pos.fill_(70 + t)
+        ctx.copy_(pos + 1)
+        graph.replay()
+        out = step(*state[1])
+        torch.cuda.synchronize()
+        assert torch.equal(out, out_g) and torch.equal(state[0][2], state[1][2])
+        assert torch.equal(state[0][0].k.view(torch.uint8), state[1][0].k.view(torch.uint8))
+    lci.get_device_status()
 
 
 # ---------------------------------------------------------------- together
