@@ -408,13 +408,18 @@ typedef struct {
  *            entries add up to H_q / num_kv_heads (0 where nothing is attended).
  * A row without an attended token is zero. Rows of d_ids may be in any order,
  * may hold -1 anywhere, and must not repeat a block. Slots that are not
- * attended are never read into a result, whatever they hold. Softmax, sums and
- * accumulation are fp32; on the tensor cores (bf16 q, head_dim 128, block_size
- * a multiple of 64, at most 16 query heads per KV head) codes are multiplied
- * exactly and softmax weights are rounded to 11 bits (row-wise schedule) or 8
- * bits (tile schedule). LCI_PHASE_PREFILL asks for the tile schedule, DECODE for
- * the row-wise one, AUTO chooses by the sizes; a call with d_mass takes the
- * row-wise one.
+ * attended are never read into a result, whatever they hold; a NaN that is
+ * attended reaches the rows that attend it and no others.
+ * Softmax, sums and accumulation are fp32. Three schedules:
+ * - tiles of queries on tcgen05 (bf16 q, head_dim 128, block_size a multiple of
+ *   64, at most 16 query heads per KV head, no d_mass, max_blocks <= 16384):
+ *   products with the exact codes; softmax weights keep 8 significant bits (at
+ *   least 2^-15 of the row's largest), query elements 2^-17 of the row's largest;
+ * - row by row on mma.sync (bf16 q, head_dim 64 or 128, block_size a multiple
+ *   of 16, at most 16 query heads per KV head): softmax weights keep 11 bits;
+ * - on CUDA cores, everything else, fp32 throughout.
+ * LCI_PHASE_PREFILL asks for the first where it fits, DECODE rules it out, AUTO
+ * chooses by an estimate from the sizes.
  * Limits: H_q a multiple of num_kv_heads, head_dim a multiple of 32 and <= 256,
  * topk <= 256, max_blocks * block_size < 2^31. Needs no workspace.
  */

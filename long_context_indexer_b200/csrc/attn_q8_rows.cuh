@@ -8,9 +8,12 @@
 // and V straight from global memory into the registers its MMA fragments need
 // (16-byte loads that cover whole 128-byte rows; the next strip is in flight
 // while one is computed), converts the codes to f16 (exact), and keeps its own
-// running maximum, sum and O. No shared memory, barrier or copy engine sits in
-// the loop, so the bytes in flight are the warps' registers (8 KiB a warp) and
-// the first load waits for nothing but the page lookup.
+// running maximum, sum and O. No barrier or copy engine sits in the loop, and the
+// first load waits for nothing but the page lookup.
+//
+// Bound: 32 rows x 32 blocks of 64 (16.8 MB) take 9.4 us, of which the strips
+// take 2.8 (6 TB/s); the rest is the chain of a launch: ids, page, first strip (2
+// us), and the merge of the warps, the cluster and the masses (2.5 us).
 //
 // Arithmetic. mma.m16n8k16, f16 in and fp32 out; the 16 rows are the group's
 // query heads. A query row is scaled by a power of two so that its largest
