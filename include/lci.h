@@ -419,7 +419,9 @@ typedef struct {
  *   of 16, at most 16 query heads per KV head): softmax weights keep 11 bits;
  * - on CUDA cores, everything else, fp32 throughout.
  * LCI_PHASE_PREFILL asks for the first where it fits, DECODE rules it out, AUTO
- * chooses by an estimate from the sizes.
+ * chooses by an estimate from the sizes. The lengths are on the device, so the
+ * estimate takes max_blocks for them: ask for PREFILL where a prompt is much
+ * shorter than the table.
  * Limits: H_q a multiple of num_kv_heads, head_dim a multiple of 32 and <= 256,
  * topk <= 256, max_blocks * block_size < 2^31. Needs no workspace.
  */
