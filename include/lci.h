@@ -485,6 +485,25 @@ LCI_API lci_status lci_cache_evict(const lci_block_table* table, int32_t batch,
                                    int32_t* d_freed, void* stream);
 
 /*
+ * One of the four entry points above with its arguments in an array, for a
+ * caller that makes the same call every step from a language whose calls cost
+ * by the argument: args holds the entry's arguments in their order, without the
+ * stream. The entry checks them as it always does.
+ */
+typedef enum {
+    LCI_CALL_KV_APPEND_Q8 = 0,
+    LCI_CALL_SPARSE_ATTN_Q8 = 1,
+    LCI_CALL_BLOCK_WEIGHT_UPDATE = 2,
+    LCI_CALL_CACHE_EVICT = 3
+} lci_call;
+typedef union {
+    void* ptr;
+    int32_t i32; /* sizes, and the enums of this header */
+    float f32;
+} lci_arg;
+LCI_API lci_status lci_call_prepared(lci_call entry, const lci_arg* args, void* stream);
+
+/*
  * lci_index_select without any device allocation. The reference pages have no
  * counterpart; this entry point exists for callers that are not allowed to
  * allocate device memory or to hold a workspace of their own: for example code

@@ -1847,4 +1847,55 @@ lci_status lci_cache_evict(const lci_block_table* table, int32_t batch, const in
     return check_launch("cache_evict");
 }
 
+lci_status lci_call_prepared(lci_call entry, const lci_arg* args, void* stream) {
+    if (!args) return fail(LCI_ERR_INVALID_ARG, "call_prepared: null pointer argument");
+    const lci_arg* a = args;
+    auto p = [&]() { return (a++)->ptr; };
+    auto i = [&]() { return (a++)->i32; };
+    auto f = [&]() { return (a++)->f32; };
+    auto ints = [&]() { return static_cast<const int32_t*>(p()); };
+    auto table = [&]() { return static_cast<const lci_block_table*>(p()); };
+    auto floats = [&]() { return static_cast<float*>(p()); };
+    // braces keep the order of evaluation that a call's arguments do not have
+    switch (static_cast<int>(entry)) {
+        case LCI_CALL_KV_APPEND_Q8: {
+            struct { void *k, *v; int dtype, batch, T; const int32_t *start, *count;
+                     const lci_block_table* t; void *kp, *vp; float *ks, *vs; }
+                x{p(), p(), i(), i(), i(), ints(), ints(), table(), p(), p(), floats(), floats()};
+            return lci_kv_append_q8(x.k, x.v, (lci_dtype)x.dtype, x.batch, x.T, x.start, x.count,
+                                    x.t, x.kp, x.vp, x.ks, x.vs, stream);
+        }
+        case LCI_CALL_SPARSE_ATTN_Q8: {
+            struct { void* q; int dtype, batch, S, H_q; void *kp, *vp; float *ks, *vs;
+                     const lci_block_table* t; const int32_t* ids; int topk;
+                     const int32_t *ctx, *q0; float scale; void* opt; int phase; void* out;
+                     float *lse, *mass; }
+                x{p(), i(), i(), i(), i(), p(), p(), floats(), floats(), table(), ints(), i(),
+                  ints(), ints(), f(), p(), i(), p(), floats(), floats()};
+            return lci_sparse_attn_q8(x.q, (lci_dtype)x.dtype, x.batch, x.S, x.H_q, x.kp, x.vp,
+                                      x.ks, x.vs, x.t, x.ids, x.topk, x.ctx, x.q0, x.scale,
+                                      static_cast<const lci_score_options*>(x.opt),
+                                      (lci_phase)x.phase, x.out, x.lse, x.mass, stream);
+        }
+        case LCI_CALL_BLOCK_WEIGHT_UPDATE: {
+            struct { const int32_t* ids; float* mass; int batch, S, H_kv, topk, nb; float decay;
+                     float* weight; }
+                x{ints(), floats(), i(), i(), i(), i(), i(), f(), floats()};
+            return lci_block_weight_update(x.ids, x.mass, x.batch, x.S, x.H_kv, x.topk, x.nb,
+                                           x.decay, x.weight, stream);
+        }
+        case LCI_CALL_CACHE_EVICT: {
+            struct { const lci_block_table* t; int batch; const int32_t* ctx; float* weight;
+                     int budget, sink, recent; void *table, *ctx_out; float* weight_out;
+                     void *kept, *freed; }
+                x{table(), i(), ints(), floats(), i(), i(), i(), p(), p(), floats(), p(), p()};
+            return lci_cache_evict(x.t, x.batch, x.ctx, x.weight, x.budget, x.sink, x.recent,
+                                   static_cast<int32_t*>(x.table), static_cast<int32_t*>(x.ctx_out),
+                                   x.weight_out, static_cast<int32_t*>(x.kept),
+                                   static_cast<int32_t*>(x.freed), stream);
+        }
+    }
+    return fail(LCI_ERR_INVALID_ARG, "call_prepared: unknown entry %d", (int)entry);
+}
+
 }  // extern "C"

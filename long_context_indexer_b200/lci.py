@@ -78,6 +78,7 @@ SIGNATURES = {
                                  _vp, _vp, _f32, _vp, _st, _vp, _vp, _vp, _vp]),
     "lci_block_weight_update": (_st, [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp]),
     "lci_cache_evict": (_st, [_vp, _i32, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "lci_call_prepared": (_st, [_st, _vp, _vp]),
     "lci_get_wait_limit_ns": (_st, [ctypes.POINTER(ctypes.c_uint64)]),
 }
 
@@ -534,9 +535,37 @@ class _ScoreOptions(ctypes.Structure):
     _fields_ = [("cap", _f32), ("d_slopes", _vp), ("d_first", _vp), ("d_last", _vp)]
 
 
-# The handle of a device's current stream, without building a stream object.
+# The handle of a device's current stream, and the current device, without
+# building an object.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+# Entry points that lci_call_prepared makes, by its lci_call.
+_PREPARED = {"lci_kv_append_q8": 0, "lci_sparse_attn_q8": 1, "lci_block_weight_update": 2,
+             "lci_cache_evict": 3}
+
+
+class _Arg(ctypes.Union):
+    _fields_ = [("ptr", _vp), ("i32", _i32), ("f32", _f32)]
+
+
+def _pack_args(name: str, args: tuple):
+    """The arguments of an entry point, without its stream, as lci_call_prepared takes them."""
+    types = SIGNATURES[name][1][:-1]
+    if len(types) != len(args):
+        raise TypeError(f"lci: {name} takes {len(types)} arguments and a stream")
+    packed = (_Arg * len(args))()
+    for slot, kind, value in zip(packed, types, args):
+        if kind is _vp:
+            slot.ptr = value.value if isinstance(value, _vp) else value
+        elif kind is _f32:
+            slot.f32 = value
+        else:
+            if not -2 ** 31 <= value < 2 ** 31:
+                raise ValueError(f"lci: {name}: {value} does not fit 32 bits")
+            slot.i32 = value
+    return packed
 
 
 class PreparedCall:
@@ -548,17 +577,20 @@ class PreparedCall:
 
     def __init__(self, name: str, args: tuple, result, device: torch.device, keep: tuple):
         self.result = result
-        self._name, self._args, self._keep = name, args, keep
-        self._fn = getattr(load_library(), name)
+        self._name, self._keep = name, keep
+        self._packed = _pack_args(name, args)
+        self._call = _PREPARED[name]
+        self._args = ctypes.addressof(self._packed)
+        self._fn = load_library().lci_call_prepared
         self._device = device.index
 
     def __call__(self, stream=None):
         raw = _raw_stream(self._device) if stream is None else stream.cuda_stream
-        if torch.cuda.current_device() == self._device:
-            rc = self._fn(*self._args, raw)
+        if _current_device() == self._device:
+            rc = self._fn(self._call, self._args, raw)
         else:
             with torch.cuda.device(self._device):
-                rc = self._fn(*self._args, raw)
+                rc = self._fn(self._call, self._args, raw)
         if rc != LCI_OK:
             _check(rc, self._name)
         return self.result
@@ -674,7 +706,7 @@ def prepare_sparse_attn_q8(q: torch.Tensor, cache: Q8Cache, table: BlockTable, i
     args = (_dev(q, "q", None, 4), _dtype_code(q), B, S, H_q, kp, vp, ks, vs, table.handle,
             _shaped(ids, "ids", torch.int32, (B, S, topk)), topk,
             _shaped(ctx_len, "ctx_len", torch.int32, (B,)),
-            _shaped(q_start, "q_start", torch.int32, (B,)), float(scale), ctypes.byref(options),
+            _shaped(q_start, "q_start", torch.int32, (B,)), float(scale), ctypes.addressof(options),
             PHASES[phase], _shaped(out, "out", q.dtype, tuple(q.shape)),
             _opt(lse, "lse", torch.float32, (B, S, H_q)),
             _opt(mass, "mass", torch.float32, (B, S, table.num_kv_heads, topk)))

@@ -162,3 +162,54 @@ def test_reference_attention_is_dense_attention():
         q[0].transpose(0, 1).double(), K.repeat_interleave(2, 0), V.repeat_interleave(2, 0), is_causal=True)
     assert torch.allclose(out[0].transpose(0, 1), want, atol=1e-12)
     assert torch.allclose(mass.sum(-1), torch.full((1, n, H), 2.0, dtype=torch.float64))
+
+
+# entry: its arguments without the stream, and changes by position that are refused
+PREPARED_CASES = {
+    "lci_kv_append_q8": (
+        lambda t: [FAKE, FAKE, 1, 2, 1, FAKE, None, t, FAKE, FAKE, FAKE, FAKE],
+        {0: None, 1: None, 2: 7, 3: 3, 4: 0, 5: None, 7: None, 8: ODD, 9: ODD, 10: None, 11: None}),
+    "lci_sparse_attn_q8": (
+        lambda t: [FAKE, 1, 2, 1, 16, FAKE, FAKE, FAKE, FAKE, t, FAKE, 4, FAKE, FAKE, 0.0, None, 0,
+                   FAKE, None, None],
+        {0: ODD, 1: 7, 2: 3, 3: -5, 4: 15, 5: ODD, 6: ODD, 7: None, 8: None, 9: None, 10: None,
+         11: 257, 12: None, 13: None, 14: math.inf, 16: 9, 17: None}),
+    "lci_block_weight_update": (
+        lambda t: [FAKE, FAKE, 2, 1, 2, 4, 8, 0.5, FAKE],
+        {0: None, 1: None, 2: 65536, 3: 0, 4: -1, 5: 257, 6: 16385, 7: -0.5, 8: None}),
+    "lci_cache_evict": (
+        lambda t: [t, 2, FAKE, FAKE, 4, 1, 1, FAKE, FAKE, FAKE, None, None],
+        {0: None, 1: 3, 2: None, 3: None, 4: 1, 5: -1, 6: 0, 7: None, 8: None, 9: None}),
+}
+
+
+@pytest.mark.parametrize("name", PREPARED_CASES)
+def test_prepared_call_passes_each_argument_in_its_place(lib, tables, name):
+    """A refused argument is refused alike, and with the same words, by both forms of the call."""
+    from long_context_indexer_b200.lci import _PREPARED, _pack_args
+    base, changes = PREPARED_CASES[name]
+    direct = getattr(lib, name)
+    messages = set()
+    for at, bad in changes.items():
+        args = base(tables["q8"])
+        args[at] = bad
+        rc = direct(*args, None)
+        words = lib.lci_last_error()
+        assert rc in (INVALID, UNSUPPORTED), (at, bad)
+        packed = _pack_args(name, tuple(args))
+        assert lib.lci_call_prepared(_PREPARED[name], ctypes.addressof(packed), None) == rc
+        assert lib.lci_last_error() == words
+        messages.add(words)
+    assert len(messages) >= 3
+
+
+def test_prepared_call_refusals(lib):
+    from long_context_indexer_b200.lci import _pack_args
+    packed = _pack_args("lci_cache_evict", tuple(PREPARED_CASES["lci_cache_evict"][0](None)))
+    assert lib.lci_call_prepared(3, None, None) == INVALID
+    assert lib.lci_call_prepared(-1, ctypes.addressof(packed), None) == INVALID
+    assert lib.lci_call_prepared(4, ctypes.addressof(packed), None) == INVALID
+    with pytest.raises(ValueError):
+        _pack_args("lci_cache_evict", (None, 2, FAKE, FAKE, 1 << 31, 1, 1, FAKE, FAKE, FAKE, None, None))
+    with pytest.raises(TypeError):
+        _pack_args("lci_cache_evict", (None, 2))
