@@ -12,8 +12,11 @@ namespace lci {
 namespace bwu {
 constexpr int kRange = 1024;   // blocks of a sequence one cluster accumulates
 constexpr int kMaxSplit = 16;  // CTAs of a cluster, each taking a share of the rows
-constexpr int kMaxWarps = 32;
-constexpr int kRowsAhead = 16;  // rows a warp loads before it adds them (one where it has one)
+constexpr int kMinWarps = 4, kMaxWarps = 32;
+constexpr int kOwn = kRange / (kMinWarps * 32);  // blocks a thread finishes
+// items (32 entries of a row) that a warp loads before it adds them: one where it
+// has one, else what the registers of 1024 threads hold
+constexpr int kAheadMany = 8;
 // the cluster's sums of this CTA's share of the blocks, and a sum per warp and block
 constexpr int kRecv = kRange + kMaxSplit;
 constexpr size_t smem_bytes(int warps) { return (size_t)warps * kRange * 4 + kRecv * 8; }
@@ -29,10 +32,12 @@ constexpr size_t smem_bytes(int warps) { return (size_t)warps * kRange * 4 + kRe
 // CTA of the cluster that finishes the block (distributed shared memory), which
 // adds the CTAs' to the weight. A sequence of more than kRange blocks is cut into
 // ranges, each with its own cluster that reads every entry and keeps those of its
-// range. Bound by latency: an 8K prompt's 2.1 MB (0.3 us of HBM) in 8.4 us, a
-// serving step of 32 sequences in 3.
+// range. Bound by latency: an 8K prompt's 2.1 MB (0.3 us of HBM) in 8.6 us, a
+// serving step of 32 sequences in 2.4. A warp's loads do not wait for one another:
+// with loads behind a test per row and KV head, 64 rows of 64 entries on 8 heads
+// took 42 us against 6.9.
 template <int kAhead>
-__global__ void __launch_bounds__(bwu::kMaxWarps * 32) block_weight_update_kernel(
+__global__ void __launch_bounds__((kAhead == 1 ? bwu::kMinWarps : bwu::kMaxWarps) * 32) block_weight_update_kernel(
     const int32_t* __restrict__ ids, const float* __restrict__ mass, int S, int H_kv, int topk,
     int nb_max, float decay, float* __restrict__ weight, int nsplit) {
     using namespace bwu;
@@ -47,63 +52,99 @@ __global__ void __launch_bounds__(bwu::kMaxWarps * 32) block_weight_update_kerne
     const int j0 = blockIdx.y * kRange;
     const int width = min(kRange, nb_max - j0);
     float* mine = hist + warp * kRange;
+    // the blocks that this CTA finishes; their weights are loaded together, ahead
+    // of everything else where registers allow it
+    const int share = (width + nsplit - 1) / nsplit;
+    const int lo = split * share, hi = min(width, lo + share);
+    float* wrow = weight + (size_t)b * nb_max + j0;
+    float old[kOwn];
+    auto load_weights = [&]() {
+#pragma unroll
+        for (int k = 0; k < kOwn; ++k) old[k] = lo + tid + k * nt < hi ? wrow[lo + tid + k * nt] : 0.f;
+    };
+    auto cta_sum = [&](int j) {
+        constexpr int kChains = kAhead == 1 ? 4 : 1;  // the warps are a multiple of 4
+        double x[kChains] = {};
+#pragma unroll 8
+        for (int w = 0; w < nw; w += kChains)
+#pragma unroll
+            for (int y = 0; y < kChains; ++y) x[y] += (double)hist[(w + y) * kRange + j];
+#pragma unroll
+        for (int y = 1; y < kChains; ++y) x[0] += x[y];
+        return x[0];
+    };
+    if constexpr (kAhead == 1) load_weights();
     for (int j = lane; j < width; j += 32) mine[j] = 0.f;
     __syncwarp();
-    const int stride = nsplit * nw;
-    const size_t step = (size_t)stride * topk;  // entries between two rows of this warp
-    for (int s0 = split * nw + warp; s0 < S; s0 += stride * kAhead) {
-        for (int i = lane; i < ((topk + 31) & ~31); i += 32) {
-            const size_t at = ((size_t)b * S + s0) * topk + i;
-            const int32_t* idp = ids + at;
-            const float* mp = mass + (((size_t)b * S + s0) * H_kv * topk + i);
-            const int rows = i < topk ? min(kAhead, (S - s0 + stride - 1) / stride) : 0;
-            int id[kAhead];
-            float add[kAhead];
+    // Items, a row's 32 entries each; this warp's are `first` and every stride-th
+    // behind it. Entries past the row, and items past the last, repeat a valid
+    // address and add nothing, so that no load waits for a branch.
+    const int chunks = (topk + 31) >> 5;
+    const long long items = (long long)S * chunks;
+    const int stride = nsplit * nw, ds = stride / chunks, dc = stride - ds * chunks;
+    const int first = split * nw + warp;
+    unsigned s = first / chunks;
+    int c = first - (int)s * chunks;
+    for (long long n0 = first; n0 < items; n0 += (long long)stride * kAhead) {
+        const int here = (int)min((long long)kAhead, (items - n0 + stride - 1) / stride);
+        int id[kAhead];
+        float add[kAhead];
+        const float* mp[kAhead];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                id[k] = k < rows ? __ldg(idp + k * step) : -1;
-                add[k] = k < rows ? __ldg(mp + k * step * H_kv) : 0.f;
-            }
-            for (int g = 1; g < H_kv; ++g) {
-                mp += topk;
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k)
-                    add[k] += k < rows ? __ldg(mp + k * step * H_kv) : 0.f;
-            }
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const unsigned at_j = (unsigned)(id[k] - j0);
-                if (at_j < (unsigned)width)
-                    mine[at_j] += add[k];
-                else if ((unsigned)id[k] + 1u > (unsigned)nb_max)
-                    raise_status(kStatusBadBlockId);
-                __syncwarp();
+        for (int k = 0; k < kAhead; ++k) {
+            const bool on = k < here;
+            const int i = 32 * c + lane, at = min(i, topk - 1);
+            const size_t row = (size_t)b * S + min(s, (unsigned)S - 1u);
+            id[k] = __ldg(ids + row * topk + at);
+            mp[k] = mass + row * H_kv * topk + at;
+            add[k] = __ldg(mp[k]);
+            if (!on || i >= topk) id[k] = -1;
+            s += ds;
+            c += dc;
+            if (c >= chunks) {
+                c -= chunks;
+                ++s;
             }
         }
+#pragma unroll kAhead == 1 ? 4 : 1
+        for (int g = 1; g < H_kv; ++g) {
+            float x[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) x[k] = __ldg(mp[k] += topk);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) add[k] += x[k];
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const unsigned at_j = (unsigned)(id[k] - j0);
+            if (at_j < (unsigned)width)
+                mine[at_j] += add[k];
+            else if ((unsigned)id[k] + 1u > (unsigned)nb_max)
+                raise_status(kStatusBadBlockId);
+            __syncwarp();
+        }
     }
+    if constexpr (kAhead > 1) load_weights();
     __syncthreads();
-    if (nsplit > 1) cluster_wait();  // every CTA of the cluster runs
-    const int share = (width + nsplit - 1) / nsplit;
-    for (int j = tid; j < width; j += nt) {
-        double x = 0.0;
-#pragma unroll 8
-        for (int w = 0; w < nw; ++w) x += (double)hist[w * kRange + j];
-        if (nsplit > 1) {
-            const int owner = j / share;
-            cg::this_cluster().map_shared_rank(recv, owner)[split * share + j - owner * share] = x;
-        } else {
-            float* w = weight + (size_t)b * nb_max + j0 + j;
-            *w = (float)((double)decay * (double)*w + x);
-        }
-    }
     if (nsplit > 1) {
+        cluster_wait();  // every CTA of the cluster runs
+        for (int j = tid; j < width; j += nt) {
+            const int owner = j / share;
+            cg::this_cluster().map_shared_rank(recv, owner)[split * share + j - owner * share] = cta_sum(j);
+        }
         cluster_arrive();
         cluster_wait();
-        for (int j = split * share + tid; j < min(width, (split + 1) * share); j += nt) {
+    }
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) {
+        const int j = lo + tid + k * nt;
+        if (j < hi) {
             double x = 0.0;
-            for (int c = 0; c < nsplit; ++c) x += recv[c * share + j - split * share];
-            float* w = weight + (size_t)b * nb_max + j0 + j;
-            *w = (float)((double)decay * (double)*w + x);
+            if (nsplit > 1)
+                for (int c = 0; c < nsplit; ++c) x += recv[c * share + j - lo];
+            else
+                x = cta_sum(j);
+            wrow[j] = (float)((double)decay * (double)old[k] + x);
         }
     }
 }

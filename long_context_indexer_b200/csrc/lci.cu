@@ -1798,27 +1798,28 @@ lci_status lci_block_weight_update(const int32_t* d_ids, const float* d_mass, in
     if (topk > lci::kMaxTopk || max_blocks > kMaxNbMax || batch > 65535)
         return fail(LCI_ERR_UNSUPPORTED, "block_weight_update: topk above %d, max_blocks above %d or "
                     "batch above 65535", lci::kMaxTopk, kMaxNbMax);
+    // A row is one item per 32 entries. Items are spread over warps, then over the
+    // CTAs of a cluster (while the grid has room), until a warp has the few that
+    // it loads at once.
+    using namespace lci::bwu;
+    const long long items = (long long)S * ((topk + 31) / 32);
+    const bool few = items <= kMinWarps;  // an item per warp
     static KernelSetup setup_one, setup_many;
-    auto one = lci::block_weight_update_kernel<1>;
-    auto many = lci::block_weight_update_kernel<lci::bwu::kRowsAhead>;
-    const bool few = S <= 4;  // a row per warp
-    const cudaError_t se = (few ? setup_one : setup_many).prepare(few ? one : many,
-            (int)lci::bwu::smem_bytes(lci::bwu::kMaxWarps), true);
-    if (se != cudaSuccess)
-        return fail(LCI_ERR_CUDA, "block_weight_update: %s", cudaGetErrorString(se));
-    // Rows are spread over warps, then over the CTAs of a cluster (while the
-    // grid has room), until a warp has the few rows it loads at once.
-    const int ranges = (max_blocks + lci::bwu::kRange - 1) / lci::bwu::kRange;
-    int warps = 4;
-    while (warps < lci::bwu::kMaxWarps && S > warps * lci::bwu::kRowsAhead) warps *= 2;
+    KernelSetup& setup = few ? setup_one : setup_many;
+    auto kern = few ? lci::block_weight_update_kernel<1> : lci::block_weight_update_kernel<kAheadMany>;
+    cudaError_t e = setup.prepare(kern, (int)smem_bytes(kMaxWarps), true);
+    const int ranges = (max_blocks + kRange - 1) / kRange;
+    int warps = kMinWarps;
+    while (warps < kMaxWarps && items > (long long)warps * kAheadMany) warps *= 2;
     int nsplit = 1;
-    while (nsplit < lci::bwu::kMaxSplit && S > nsplit * warps * lci::bwu::kRowsAhead &&
+    while (nsplit < kMaxSplit && items > (long long)nsplit * warps * kAheadMany &&
            2ll * nsplit * ranges * batch <= 148)
         nsplit *= 2;
-    const cudaError_t e = launch_early(
-        few ? one : many, dim3((unsigned)nsplit, (unsigned)ranges, (unsigned)batch),
-        dim3((unsigned)warps * 32), lci::bwu::smem_bytes(warps), static_cast<cudaStream_t>(stream),
-        nsplit, d_ids, d_mass, S, num_kv_heads, topk, max_blocks, decay, d_weight, nsplit);
+    if (e == cudaSuccess)
+        e = launch_early(kern, dim3((unsigned)nsplit, (unsigned)ranges, (unsigned)batch),
+                         dim3((unsigned)warps * 32), smem_bytes(warps),
+                         static_cast<cudaStream_t>(stream), nsplit, d_ids, d_mass, S, num_kv_heads,
+                         topk, max_blocks, decay, d_weight, nsplit);
     if (e != cudaSuccess) return fail(LCI_ERR_CUDA, "block_weight_update: %s", cudaGetErrorString(e));
     return check_launch("block_weight_update");
 }

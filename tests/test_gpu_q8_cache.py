@@ -470,6 +470,27 @@ def test_block_weights_accumulate(B, S, H, topk, NB, decay):
     assert torch.equal(got, again)
 
 
+@pytest.mark.parametrize("B,S,H,topk,NB", [(1, 4, 8, 32, 1024), (2, 2, 3, 33, 1025), (1, 38, 2, 97, 104), (3, 73, 4, 256, 300),
+                                           (2, 300, 8, 64, 2048), (1, 1100, 2, 200, 1200)])
+def test_block_weights_of_wide_rows_and_many_heads(B, S, H, topk, NB):
+    """Rows of several runs of 32 entries, masses of many heads, and -1 entries whose masses do not count."""
+    g = torch.Generator().manual_seed(7)
+    ids = random_ids(B, S, NB, topk, g)
+    ids[torch.rand(ids.shape, generator=g) < 0.2] = -1
+    mass = torch.rand(B, S, H, topk, generator=g) ** 6
+    mass[(ids < 0)[:, :, None, :].expand_as(mass)] = float("nan")
+    weight = torch.rand(B, NB, generator=g)
+    got = lci.block_weight_update(weight.cuda(), ids.cuda(), mass.cuda(), decay=0.5)
+    again = lci.block_weight_update(weight.cuda(), ids.cuda(), mass.cuda(), decay=0.5)
+    torch.cuda.synchronize()
+    lci.get_device_status()
+    mass[mass != mass] = 0.0
+    want = ref.weight_update(weight, ids, mass, 0.5)
+    tol = want * 2.0 ** -24 * (H + 2 + S) + 1e-30
+    assert ((got.cpu().double() - want).abs() <= tol).all()
+    assert torch.equal(got, again)
+
+
 def test_block_weights_flag_bad_ids():
     ids = torch.tensor([[[0, 7, -1, -3]]], dtype=torch.int32, device="cuda")
     w = lci.block_weight_update(torch.zeros(1, 4, device="cuda"), ids, torch.ones(1, 1, 1, 4, device="cuda"))
