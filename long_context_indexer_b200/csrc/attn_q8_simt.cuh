@@ -1,14 +1,18 @@
 // attn_q8_simt.cuh -- attention over the 8-bit paged cache on CUDA cores (fp32
 // math): fp32 queries and every shape the tensor-core kernels do not cover.
 //
-// One CTA per (query row, KV head); the query heads of the group one after the
-// other. The warps take the row's selected blocks in turn; inside a block a
-// lane computes the logit of one token (its 16-byte runs of K against the query
-// in shared memory), the warp folds 32 tokens into an online softmax, and for
-// P V the lanes split the head dim. The warps' (max, sum, O) merge through
-// shared memory. Bound by instruction issue: about two conversions and four
-// multiply-adds per four cached elements.
+// One CTA per (query row, query head). Where masses are asked for, the heads of a
+// KV head share a cluster of up to 8 CTAs, which adds the heads' masses through
+// distributed shared memory, in order. The warps take the row's selected blocks
+// in turn; inside a block a lane computes the logit of one token (its 16-byte
+// runs of K against the query in shared memory), the warp folds 32 tokens into an
+// online softmax, and for P V the lanes split the head dim. The warps' (max, sum,
+// O) merge through shared memory. Bound by instruction issue: about two
+// conversions and four multiply-adds per four cached elements (32 rows x 16 heads
+// x 32 blocks of 64, fp32: 131 us; with a row's heads in one CTA 1452).
 #pragma once
+
+#include <cooperative_groups.h>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -107,11 +111,12 @@ __device__ __forceinline__ float q8_score(float z, float cap, float inv_cap, flo
 }
 
 constexpr int kQ8SimtWarps = 4;
+constexpr int kQ8SimtCluster = 8;  // CTAs that share a KV head's masses
 constexpr int kQ8MaxHd = 256;
 
 // HD: the largest head_dim of the instance (64, 128 or 256).
 template <typename T, int HD>
-__global__ void __launch_bounds__(kQ8SimtWarps * 32) sparse_attn_q8_simt_kernel(const AttnQ8Args a) {
+__global__ void __launch_bounds__(kQ8SimtWarps * 32) sparse_attn_q8_simt_kernel(const AttnQ8Args a, int heads, int parts) {
     constexpr int kPer = HD / 32;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     float* sq = reinterpret_cast<float*>(smem_raw);                                // [hd] query, fp32
@@ -122,8 +127,9 @@ __global__ void __launch_bounds__(kQ8SimtWarps * 32) sparse_attn_q8_simt_kernel(
     float* bt = br + a.topk;                       // [topk] mass over the group's heads
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row = blockIdx.x, g = blockIdx.y;
+    const int part = blockIdx.x % parts, row = blockIdx.x / parts, g = blockIdx.y;
     const int G = a.H_q / a.H_kv, hd = a.hd, bs = a.bs;
+    const int h0 = part * heads, h1 = min(G, h0 + heads);  // this CTA's heads of the group
     const int b = row / a.S, s = row - b * a.S;
     const int per_lane = hd >> 5;
     const Q8Window win = q8_window(a, row, b, s);
@@ -132,7 +138,7 @@ __global__ void __launch_bounds__(kQ8SimtWarps * 32) sparse_attn_q8_simt_kernel(
     if (a.mass)
         for (int i = tid; i < a.topk; i += blockDim.x) bt[i] = 0.f;
 
-    for (int hl = 0; hl < G; ++hl) {
+    for (int hl = h0; hl < h1; ++hl) {
         const int h = g * G + hl;
         const T* qh = static_cast<const T*>(a.q) + ((size_t)row * a.H_q + h) * hd;
         __syncthreads();  // the previous head's merge has read sq and so
@@ -249,7 +255,18 @@ __global__ void __launch_bounds__(kQ8SimtWarps * 32) sparse_attn_q8_simt_kernel(
     }
     if (a.mass) {
         float* mrow = a.mass + ((size_t)row * a.H_kv + g) * a.topk;
-        for (int i = tid; i < a.topk; i += blockDim.x) mrow[i] = bt[i];
+        if (parts > 1) {
+            namespace cg = cooperative_groups;
+            cg::this_cluster().sync();
+            for (int i = part * blockDim.x + tid; i < a.topk; i += parts * blockDim.x) {
+                float sum = 0.f;
+                for (int p = 0; p < parts; ++p) sum += *cg::this_cluster().map_shared_rank(bt + i, p);
+                mrow[i] = sum;
+            }
+            cg::this_cluster().sync();  // no CTA leaves while its masses are read
+        } else {
+            for (int i = tid; i < a.topk; i += blockDim.x) mrow[i] = bt[i];
+        }
     }
 }
 

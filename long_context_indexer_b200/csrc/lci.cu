@@ -1460,11 +1460,22 @@ template <typename T>
 lci_status launch_attn_q8_simt(const lci::AttnQ8Args& a, int32_t batch, cudaStream_t st) {
     const size_t smem = (size_t)(a.hd * (1 + lci::kQ8SimtWarps) + 2 * lci::kQ8SimtWarps +
                                  3 * a.topk) * 4;
-    const dim3 grid((unsigned)(batch * a.S), (unsigned)a.H_kv);
+    // A CTA per query head; where masses are asked for, the heads of a KV head in a
+    // cluster of up to 8 CTAs, which adds theirs up.
+    const int G = a.H_q / a.H_kv;
+    const long long rows = (long long)batch * a.S;
+    int heads = a.mass ? (G + lci::kQ8SimtCluster - 1) / lci::kQ8SimtCluster : 1;
+    int parts = (G + heads - 1) / heads;
+    if (rows * parts >= (1ll << 31)) {
+        heads = G;
+        parts = 1;
+    }
+    const dim3 grid((unsigned)(rows * parts), (unsigned)a.H_kv);
     auto kern = a.hd <= 64 ? lci::sparse_attn_q8_simt_kernel<T, 64>
                            : a.hd <= 128 ? lci::sparse_attn_q8_simt_kernel<T, 128>
                                          : lci::sparse_attn_q8_simt_kernel<T, 256>;
-    const cudaError_t e = launch_early(kern, grid, dim3(lci::kQ8SimtWarps * 32), smem, st, 1, a);
+    const cudaError_t e = launch_early(kern, grid, dim3(lci::kQ8SimtWarps * 32), smem, st,
+                                       a.mass ? parts : 1, a, heads, parts);
     if (e != cudaSuccess) return fail(LCI_ERR_CUDA, "sparse_attn_q8: %s", cudaGetErrorString(e));
     return check_launch("sparse_attn_q8");
 }

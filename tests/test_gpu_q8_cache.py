@@ -450,6 +450,24 @@ def test_refusals_of_the_binding():
         lci.sparse_attn_workspace_size(2, 1, 16, 4, bt)
 
 
+@pytest.mark.parametrize("dtype,H,G,hd,bs,topk", [(torch.float32, 2, 11, 64, 16, 5), (torch.float32, 1, 8, 96, 48, 3),
+                                                  (torch.bfloat16, 2, 17, 128, 64, 4), (torch.float32, 1, 40, 32, 8, 256),
+                                                  (torch.bfloat16, 1, 3, 256, 24, 7)])
+@pytest.mark.parametrize("mass", [False, True])
+def test_cuda_core_schedule_with_many_heads(dtype, H, G, hd, bs, topk, mass):
+    """The heads of a KV head over CTAs, their masses added up across them."""
+    lens = [topk * bs + 3, bs - 1]
+    B, S = 2, 3
+    cache, table, cpu = filled_cache(B, H, bs, hd, lens, 31)
+    g = torch.Generator().manual_seed(32)
+    NB = table.shape[1]
+    ids = random_ids(B, S, NB, topk, g)
+    q = torch.randn(B, S, H * G, hd, generator=g).to(dtype)
+    ctx = torch.tensor(lens, dtype=torch.int32)
+    check_attention(q, cache, table, cpu, bs, ids, ctx, (ctx - S).clamp(min=0).to(torch.int32), mass=mass,
+                    cap=20.0, slopes=torch.rand(H * G, generator=g) / 8)
+
+
 # ---------------------------------------------------------------- weights and eviction
 
 @pytest.mark.parametrize("B,S,H,topk,NB,decay", [(1, 1, 1, 1, 1, 1.0), (3, 1, 2, 8, 40, 0.5), (2, 70, 1, 32, 100, 1.0),
