@@ -32,8 +32,8 @@ constexpr size_t smem_bytes(int warps) { return (size_t)warps * kRange * 4 + kRe
 // CTA of the cluster that finishes the block (distributed shared memory), which
 // adds the CTAs' to the weight. A sequence of more than kRange blocks is cut into
 // ranges, each with its own cluster that reads every entry and keeps those of its
-// range. Bound by latency: an 8K prompt's 2.1 MB (0.3 us of HBM) in 8.6 us, a
-// serving step of 32 sequences in 2.4. A warp's loads do not wait for one another:
+// range. Bound by latency: an 8K prompt's 2.1 MB (0.3 us of HBM) in 8.7 us, a
+// serving step of 32 sequences in 2.3. A warp's loads do not wait for one another:
 // with loads behind a test per row and KV head, 64 rows of 64 entries on 8 heads
 // took 42 us against 6.9.
 template <int kAhead>
@@ -185,7 +185,7 @@ __device__ __forceinline__ int cta_exclusive_sum(int v, int* scratch, int& total
 // every block its place: kept blocks, then freed ones, then the rest of the row,
 // each in order. Every input is read before a barrier of the cluster that
 // precedes the first write, so outputs may be the inputs. Bound by the latency
-// of that chain (five cluster barriers); one CTA for all 16384 blocks of a
+// of that chain (a cluster barrier per digit and per prefix); one CTA for all 16384 blocks of a
 // sequence was bound by its instructions (28 us against 12 for 8 sequences).
 template <int IPT>
 __global__ void __launch_bounds__(1024) cache_evict_kernel(

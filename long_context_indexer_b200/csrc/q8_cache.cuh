@@ -196,7 +196,9 @@ constexpr int kAppendHold = 2;  // runs of new K, and of new V, a thread holds
 //
 // Bound by HBM for a prompt: K and V of a cell are loaded together so that a
 // CTA has 32 KiB in flight behind one chain of lookups, and holding raw bf16
-// instead of floats keeps four CTAs on an SM.
+// instead of floats keeps four CTAs on an SM (4 x 8191 tokens of 8 heads behind 1003:
+// 36.8 us, 84 % of a measured copy; a ragged batch of 140.9 MB 29.5 us, 73 %; one
+// token of 32 sequences 2.5 us, the chain of its loads).
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kAppendMaxThreads, sizeof(T) == 2 ? 4 : 2) kv_append_q8_kernel(
     const T* __restrict__ k_new, const T* __restrict__ v_new, int T_new, int H_kv, int hd, int bs,
