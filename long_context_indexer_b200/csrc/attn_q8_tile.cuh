@@ -608,6 +608,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
             if (!warp_any) {
                 // nothing of the unit concerns these rows: pass the references on, P = 0
                 if (u > 0) tile_wait(their_dec, (grp == 0 ? k - 1 : k) & 1, s_abort);
+                __syncwarp();  // every lane has seen the phase: once passed on, it can be followed by two more
                 if (lane == 0) mbar_arrive(my_dec);
                 tile_wait(&sfull[slot], turn & 1, s_abort);
                 tc_fence_after();

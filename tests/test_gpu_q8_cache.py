@@ -640,3 +640,24 @@ def test_a_bounded_decode_loop():
         assert torch.equal(table.cpu(), want[0]) and torch.equal(ctx.cpu(), want[1]) and torch.equal(weight.cpu(), want[2])
         evicted += int(freed.sum())
     assert evicted > 0 and sorted(table.flatten().tolist()) == list(range(P))
+
+
+def test_tiles_whose_queries_share_no_block():
+    """Every query picks blocks of its own, so that most of a tile's warps only
+    pass the softmax references on: many rounds of the same call give the same."""
+    g = torch.Generator().manual_seed(120)
+    B, S, G, bs, hd, topk = 1, 48, 16, 64, 128, 6
+    NB = S * topk
+    cache, table, cpu = filled_cache(B, 1, bs, hd, [NB * bs], 121)
+    q = torch.randn(B, S, G, hd, generator=g).to(torch.bfloat16)
+    ids = torch.randperm(NB, generator=g).reshape(1, S, topk).to(torch.int32)
+    ctx = torch.tensor([NB * bs], dtype=torch.int32)
+    args = (q, cache, table, cpu, bs, ids, ctx, ctx - S)
+    first = check_attention(*args, phase="prefill", mass=False, p_bits=8)
+    bt = lci.create_block_table(table.cuda(), cache.k)
+    call = lci.prepare_sparse_attn_q8(q.cuda(), cache, bt, ids.cuda(), ctx.cuda(), (ctx - S).cuda(), phase="prefill")
+    for _ in range(50):
+        call()
+    torch.cuda.synchronize()
+    lci.get_device_status()
+    assert torch.equal(call.result.cpu().double(), first)
