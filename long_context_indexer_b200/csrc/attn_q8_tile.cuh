@@ -152,6 +152,18 @@ __device__ __forceinline__ void tile_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
+// Waits for copies or MMAs of this CTA that are under way, before what they read
+// or write is given up: at least 2 s, however short the limit of other waits is.
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+    const unsigned long long t0 = global_ns();
+    const unsigned long long limit = max(g_wait_limit_ns, 2000000000ull);
+    while (!mbar_try_wait(bar, parity))
+        if (global_ns() - t0 > limit) {
+            raise_status(kStatusTimeout);
+            return;
+        }
+}
+
 // One query row and head by one warp, fp32, reading only attended tokens
 // (sq: hd floats of shared memory of this warp).
 __device__ __noinline__ void q8_row_by_warp(const AttnQ8Args& a, int row, int h, float* sq) {
@@ -515,7 +527,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
             // nothing of this thread may still run on the tensor core when the
             // TMEM is released
             tc_commit(&drain[0]);
-            mbar_wait(&drain[0], 0);
+            drain_wait(&drain[0], 0);
         }
     } else if (warp == 2) {
         // ---------------- O += P V ----------------
@@ -544,7 +556,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                 tc_commit(&vempty[vs]);
             }
             tc_commit(&drain[1]);  // the epilogue waits for it too
-            mbar_wait(&drain[1], 0);
+            drain_wait(&drain[1], 0);
         }
     } else {
         // ---------------- softmax and epilogue: a thread per row and group ----------------
@@ -795,15 +807,24 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         const float m_end = mref[r];
         if (m_end != m) l *= fast_exp2(m - m_end);
         lsum[grp * 128 + r] = l;
-        named_barrier_sync(kEndBarrier, kEndThreads);
         tile_wait(&drain[1], 0, s_abort);
+        named_barrier_sync(kEndBarrier, kEndThreads);
         tc_fence_after();
+        // no role waits for anything any more: the same for every thread
+        const bool gave_up = *s_abort != 0;
         float L = 0.f;
 #pragma unroll
         for (int k = 0; k < kGroups; ++k) L += lsum[k * 128 + r];
-        if (*s_abort) L = 0.f;
+        if (gave_up) L = 0.f;
         const float inv = 1.f / L;
         if (a.lse && real && grp == 0) a.lse[qrow] = L == 0.f ? -INFINITY : m_end - kShift + log2f(L);
+        __nv_bfloat16* o0 = static_cast<__nv_bfloat16*>(a.out) + (((size_t)b * a.S + s0) * a.H_q + (size_t)g * G) * kHD;
+        if (gave_up) {
+            // zeros, not through the K ring: copies into it may still be under way
+            if (real)
+                for (int c = grp; c < kHD / 8; c += kGroups)
+                    *reinterpret_cast<uint4*>(o0 + ((size_t)qi * a.H_q + (r - qi * G)) * kHD + 8 * c) = make_uint4(0, 0, 0, 0);
+        } else {
         // through the K ring (every copy and MMA of it is done), rows padded by 16
         // bytes, so that rows leave whole
         constexpr int kPitch = 2 * kHD + 16;
@@ -828,7 +849,6 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         if (real && bad) redo[r] = 1;
         named_barrier_sync(kEndBarrier, kEndThreads);
         const uint32_t inv_g = (65536u + G - 1) / G;
-        __nv_bfloat16* o0 = static_cast<__nv_bfloat16*>(a.out) + (((size_t)b * a.S + s0) * a.H_q + (size_t)g * G) * kHD;
         for (int x = tid - 32 * kFirstSoftmax; x < kRows * 16; x += kEndThreads) {
             const int row = x >> 4, c = x & 15, q = (int)((row * inv_g) >> 16);
             if (q < QT && s0 + q < a.S)
@@ -839,11 +859,11 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
         const bool again = __any_sync(0xffffffffu, redo[lane] | redo[lane + 32] | redo[lane + 64] | redo[lane + 96]);
         if (again) {
             named_barrier_sync(kEndBarrier, kEndThreads);  // all rows have left the K ring
-            if (!*s_abort)
-                for (int x = warp - kFirstSoftmax; x < QT * G; x += kGroups * kGroupWarps)
-                    if (redo[x] && s0 + x / G < a.S)
-                        q8_row_by_warp(a, b * a.S + s0 + x / G, g * G + x % G,
-                                       reinterpret_cast<float*>(smem + kOffK) + warp * kHD);
+            for (int x = warp - kFirstSoftmax; x < QT * G; x += kGroups * kGroupWarps)
+                if (redo[x] && s0 + x / G < a.S)
+                    q8_row_by_warp(a, b * a.S + s0 + x / G, g * G + x % G,
+                                   reinterpret_cast<float*>(smem + kOffK) + warp * kHD);
+        }
         }
     }
     tc_fence_before();
@@ -857,7 +877,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
     // a tile that gave up: its copies still land before the CTA's memory is reused
     if (*s_abort && lane == 0 && (warp == 0 || warp == 3))
         for (int i = max(0, issued - kStages); i < issued; ++i)
-            mbar_wait(&(warp == 0 ? kfull : vfull)[i & (kStages - 1)], (i / kStages) & 1);
+            drain_wait(&(warp == 0 ? kfull : vfull)[i & (kStages - 1)], (i / kStages) & 1);
 }
 
 }  // namespace lci

@@ -661,3 +661,33 @@ def test_tiles_whose_queries_share_no_block():
     torch.cuda.synchronize()
     lci.get_device_status()
     assert torch.equal(call.result.cpu().double(), first)
+
+
+def test_tiles_that_give_up_leave_zeros():
+    """With a limit that nearly every wait exceeds, tiles give up: each of their rows
+    is zero, or what it should be where the tile got through, and never raw codes."""
+    q, cache, table, cpu, bs, ids, ctx_len, q_start = attention_inputs(SHAPES[5], 130)
+    bt = lci.create_block_table(table.cuda(), cache.k)
+    dev = [t.cuda() for t in (q, ids, ctx_len, q_start)]
+    call = lci.prepare_sparse_attn_q8(dev[0], cache, bt, *dev[1:], phase="prefill", lse=True)
+    want = [t.clone() for t in call()]
+    default = lci.get_wait_limit_ns()
+    lci.set_wait_limit_ns(1)
+    try:
+        for _ in range(5):
+            for t in call.result:
+                t.fill_(7.0)
+            call()
+            try:
+                lci.get_device_status()
+                timed_out = False
+            except lci.LciError as e:
+                assert e.status == 6
+                timed_out = True
+            zero = (call.result[0] == 0).all(-1) & (call.result[1] == -float("inf"))
+            same = (call.result[0] == want[0]).all(-1) & (call.result[1] == want[1])
+            assert (zero | same).all() and (timed_out or same.all())
+    finally:
+        lci.set_wait_limit_ns(default)
+    assert all(torch.equal(a, b) for a, b in zip(call(), want))
+    lci.get_device_status()
