@@ -583,8 +583,12 @@ class PreparedCall:
         self._args = ctypes.addressof(self._packed)
         self._fn = load_library().lci_call_prepared
         self._device = device.index
+        # the packed handle dangles once its table is closed
+        self._table = next((t for t in keep if isinstance(t, BlockTable)), None)
 
     def __call__(self, stream=None):
+        if self._table is not None and self._table._handle is None:
+            raise ValueError(f"lci: {self._name}: the block table was closed")
         raw = _raw_stream(self._device) if stream is None else stream.cuda_stream
         if _current_device() == self._device:
             rc = self._fn(self._call, self._args, raw)
@@ -875,6 +879,8 @@ class SparseDecodeStep:
     def __call__(self, stream=None) -> None:
         """Launch the step on its stream, or on `stream` if given (e.g. the
         stream a CUDA graph is being captured on)."""
+        if self._keep[-1]._handle is None:
+            raise ValueError(f"lci: {self._name}: the block table was closed")
         args = self._args if stream is None else self._args[:-1] + (_stream(stream),)
         rc = self._fn(*args)
         if rc != LCI_OK:

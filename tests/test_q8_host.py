@@ -213,3 +213,38 @@ def test_prepared_call_refusals(lib):
         _pack_args("lci_cache_evict", (None, 2, FAKE, FAKE, 1 << 31, 1, 1, FAKE, FAKE, FAKE, None, None))
     with pytest.raises(TypeError):
         _pack_args("lci_cache_evict", (None, 2))
+
+
+def _table(lib):
+    t = object.__new__(lci.BlockTable)  # a handle over no device memory
+    t._handle, t._lib = ctypes.c_void_p(), lib
+    assert lib.lci_create_block_table(FAKE, 2, 4, 8, 64, 2, 128, 2, ctypes.byref(t._handle)) == 0
+    return t
+
+
+class _Stream:
+    cuda_stream = None
+
+
+def test_calls_prepared_over_a_closed_table_are_refused(lib, monkeypatch):
+    import long_context_indexer_b200.lci as binding
+    made = []
+    monkeypatch.setattr(binding, "_current_device", lambda: 0)
+    t = _table(lib)
+    args = (t.handle, 2, FAKE, FAKE, 4, 1, 1, FAKE, FAKE, FAKE, None, None)
+    call = binding.PreparedCall("lci_cache_evict", args, None, torch.device("cuda", 0), (t,))
+    call._fn = lambda *a: made.append(a) or 0
+    call(_Stream)
+    assert len(made) == 1
+    t.close()
+    with pytest.raises(ValueError, match="closed"):
+        call(_Stream)
+    step = object.__new__(lci.SparseDecodeStep)
+    step._name, step._keep, step._args = "lci_sparse_decode", (_table(lib),), (None,)
+    step._fn = lambda *a: made.append(a) or 0
+    step()
+    assert len(made) == 2
+    step._keep[-1].close()
+    with pytest.raises(ValueError, match="closed"):
+        step()
+    assert len(made) == 2
