@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+import weakref
 from typing import Dict, Optional, Tuple
 
 import torch
@@ -171,6 +172,10 @@ def workspace(device: torch.device, nbytes: int, tag: str) -> torch.Tensor:
 
 # ---------------------------------------------------------------- block table
 
+def _closed_table(*args):
+    raise ValueError("lci: the block table of this prepared call was closed")
+
+
 class BlockTable:
     """Owns an lci_block_table handle; keeps the table tensor alive."""
 
@@ -199,7 +204,17 @@ class BlockTable:
         _check(self._lib.lci_validate_block_table(self._handle, _stream(stream)),
                "lci_validate_block_table")
 
+    _prepared = None  # the calls that hold the handle
+
+    def register(self, call) -> None:
+        """``call`` holds the handle in its prepared arguments: close() makes it refuse."""
+        if self._prepared is None:
+            self._prepared = weakref.WeakSet()
+        self._prepared.add(call)
+
     def close(self) -> None:
+        for call in self._prepared or ():
+            call._fn = _closed_table
         if getattr(self, "_handle", None):
             self._lib.lci_destroy_block_table(self._handle)
             self._handle = None
@@ -583,12 +598,11 @@ class PreparedCall:
         self._args = ctypes.addressof(self._packed)
         self._fn = load_library().lci_call_prepared
         self._device = device.index
-        # the packed handle dangles once its table is closed
-        self._table = next((t for t in keep if isinstance(t, BlockTable)), None)
+        for t in keep:
+            if isinstance(t, BlockTable):
+                t.register(self)
 
     def __call__(self, stream=None):
-        if self._table is not None and self._table._handle is None:
-            raise ValueError(f"lci: {self._name}: the block table was closed")
         raw = _raw_stream(self._device) if stream is None else stream.cuda_stream
         if _current_device() == self._device:
             rc = self._fn(self._call, self._args, raw)
@@ -866,6 +880,7 @@ class SparseDecodeStep:
         self._keep = (q_c, k_c, ctx_len, q_start, q, k_pool, v_pool, table)
         self._name = "lci_sparse_decode_persistent" if persistent else "lci_sparse_decode"
         self._fn = getattr(load_library(), self._name)
+        table.register(self)
         self._stream = _stream(stream)
         self._args = (
             _dev(q_c, "q_c", None, 4), _dev(k_c, "k_c", q_c.dtype, 4), _dtype_code(q_c), B, S, H_i,
@@ -879,8 +894,6 @@ class SparseDecodeStep:
     def __call__(self, stream=None) -> None:
         """Launch the step on its stream, or on `stream` if given (e.g. the
         stream a CUDA graph is being captured on)."""
-        if self._keep[-1]._handle is None:
-            raise ValueError(f"lci: {self._name}: the block table was closed")
         args = self._args if stream is None else self._args[:-1] + (_stream(stream),)
         rc = self._fn(*args)
         if rc != LCI_OK:

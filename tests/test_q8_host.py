@@ -242,6 +242,7 @@ def test_calls_prepared_over_a_closed_table_are_refused(lib, monkeypatch):
     step = object.__new__(lci.SparseDecodeStep)
     step._name, step._keep, step._args = "lci_sparse_decode", (_table(lib),), (None,)
     step._fn = lambda *a: made.append(a) or 0
+    step._keep[-1].register(step)  # as its constructor, which needs a GPU's tensors, does
     step()
     assert len(made) == 2
     step._keep[-1].close()
