@@ -413,11 +413,15 @@ typedef struct {
  * Softmax, sums and accumulation are fp32. Three schedules:
  * - tiles of queries on tcgen05 (bf16 q, head_dim 128, block_size a multiple of
  *   64, at most 16 query heads per KV head, no d_mass, max_blocks <= 16384):
- *   products with the exact codes; softmax weights keep 8 significant bits (at
- *   least 2^-15 of the row's largest), query elements 2^-17 of the row's largest;
+ *   products with the exact codes; softmax weights keep 8 significant bits, query
+ *   elements 2^-17 of the row's largest;
  * - row by row on mma.sync (bf16 q, head_dim 64 or 128, block_size a multiple
  *   of 16, at most 16 query heads per KV head): softmax weights keep 11 bits;
  * - on CUDA cores, everything else, fp32 throughout.
+ * Weights that are rounded so are those of the codes, softmax weight * v scale;
+ * ones below 2^-14 of a row's largest keep fewer bits and are off by at most 2^-25
+ * of the largest. The row's sum counts every weight unrounded. The v scales of the
+ * blocks that a row attends lie within 2^96 of each other.
  * LCI_PHASE_PREFILL asks for the first where it fits, DECODE rules it out, AUTO
  * chooses by an estimate from the sizes. The lengths are on the device, so the
  * estimate takes max_blocks for them: ask for PREFILL where a prompt is much

@@ -10,22 +10,26 @@
 // stored and are the 8-bit B operands of tcgen05.mma.kind::f8f6f4. The 16-bit
 // side is split instead. A bf16 query element, scaled by a power of two per row,
 // is the sum of two e4m3 numbers (4 + 4 significant bits, exact down to 2^-17 of
-// the row's largest element), and a softmax weight is rounded to such a sum (8
-// significant bits, the precision of a bf16 weight, down to 2^-15 of the row's
-// largest weight). Both products take two MMAs at twice the bf16 rate: the same
-// tensor time as a bf16 cache, half its shared-memory traffic, and no
-// conversion of 64 KiB per pair.
-//   S  = Qhi K^T + Qlo K^T   M=128, N=128 tokens, A = Q from shared memory
-//   O += Phi V   + Plo V     M=128, N=128 dims, K=64 tokens, A = P from TMEM,
-//                            B = V MN-major from shared memory
-// (Q stays out of TMEM so that three pairs of S fit beside O.)
+// the row's largest element). A softmax weight is the sum of three e5m2 numbers:
+// rounded to f16, its upper byte is one, the upper byte of the rest another, and
+// what is left is rounded to a third (3 + 3 + 3 bits, off by at most 2^-8.6 of it).
+// e5m2 has f16's exponents, so this holds down to 2^-16 of the row's reference,
+// and smaller weights are off by at most 2^-25 of it: a row keeps the many small
+// weights behind one large one. Two e4m3 parts, which end at 2^-9, lost all of
+// them below 2^-15 of the largest.
+//   S  = Qhi K^T + Qlo K^T       M=128, N=128 tokens, A = Q from shared memory
+//   O += P0 V + P1 V + P2 V      M=128, N=128 dims, K=64 tokens, A = P from TMEM,
+//                                B = V MN-major from shared memory
+// (Q stays out of TMEM so that three pairs of S fit beside O.) The third part
+// costs 8 % (8K prompt). V converted to f16 for two-byte weights was slower: by
+// the softmax warps 351 us, by warps of their own 325 to 429, against 300.
 //
 // Scales. A block's k scale multiplies the fp32 logits. Its v scale enters the
 // exponent, so that the weight is that of the codes, p = 2^(x + log2 vs - m),
 // and the row sum adds p / vs; the running reference m of a row is the maximum
-// of x + log2 vs. Weights are 2^5 at the reference; it moves only when a unit
-// passes it by more than 3.75 (weights stay below 448), and O is rescaled only
-// then.
+// of x + log2 vs. Weights are 2^8 at the reference; it moves only when a unit
+// passes it by more than 7.75 (weights stay below 57344, e5m2's largest), and O is
+// rescaled only then (with 3.75: 317 us against 300).
 //
 // Warps: 0 copies K and 3 copies V (K runs ahead of the V ring, whose stages free
 // only after the softmax), 1 issues Q K^T, 2 issues P V (the waits and commits
@@ -77,10 +81,11 @@ constexpr int kFirstSoftmax = 4;       // warps 0..3: K copies, Q K^T, P V, V co
 constexpr int kThreads = 32 * kFirstSoftmax + kGroups * 32 * kGroupWarps;
 constexpr int kSlots = 3;              // pairs of S in flight
 // TMEM columns: O fp32, kSlots pairs of S (fp32; a unit's 64 columns then hold
-// its P as 16 columns of high and 16 of low parts)
+// its P: for each half of the unit's tokens 8 columns of each part)
 constexpr int kColO = 0, kColS = 128, kTmemCols = 512;
-constexpr float kShift = 5.f;          // log2 of the weight at the reference
-constexpr float kLazy = 3.75f;         // 2^(5 + 3.75) < 448
+constexpr int kParts = 3;              // e5m2 parts of a weight
+constexpr float kShift = 8.f;          // log2 of the weight at the reference
+constexpr float kLazy = 7.75f;         // 2^(8 + 7.75) < 57344, the largest e5m2
 // shared memory (offsets from a 1024-byte aligned base)
 constexpr int kOffK = 0;
 constexpr int kOffV = kOffK + kStages * kStageBytes;
@@ -91,9 +96,10 @@ constexpr int kOffWin = kOffUnion + kUnionBytes;    // [kMaxQT] Q8Window
 constexpr int kOffBar = kOffWin + kMaxQT * 16;
 constexpr int kOffRow = kOffBar + 512;              // [128] references, [kGroups][128] sums, [128] flags, [128] factors
 constexpr int kSmemBytes = kOffRow + (3 + kGroups) * 128 * 4 + 1024 /*alignment slack*/;
-// instruction descriptors, kind::f8f6f4: D fp32, A and B e4m3, M = 128, N = 128
+// instruction descriptors, kind::f8f6f4: D fp32, A and B e4m3 (P V: A e5m2, B
+// MN-major), M = 128, N = 128
 constexpr uint32_t kIdescQK = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);  // B MN-major
+constexpr uint32_t kIdescPV = kIdescQK | (1u << 7) | (1u << 16);
 }  // namespace q8t
 
 // D (+)= A B, 8-bit operands, A read from TMEM (4 elements per column).
@@ -114,26 +120,33 @@ __device__ __forceinline__ void tc_mma_f8(uint32_t tmem_d, uint64_t a, uint64_t 
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
 }
 
-// Two f16x2 -> four e4m3 codes.
-__device__ __forceinline__ uint32_t f16x4_to_e4m3(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 s, t;\n\tcvt.rn.satfinite.e4m3x2.f16x2 s, %1;\n\t"
-        "cvt.rn.satfinite.e4m3x2.f16x2 t, %2;\n\tmov.b32 %0, {s, t};\n\t}"
-        : "=r"(r)
-        : "r"(a), "r"(b));
-    return r;
+// Four non-negative weights (below 57344) -> the e5m2 codes of three parts that
+// add up to them. A weight is rounded to f16 (11 bits); an e5m2 number is the
+// upper byte of an f16, so the upper byte is a part of 3 bits and subtracting it
+// is exact, twice; the rest is rounded to 3 bits.
+__device__ __forceinline__ void split_weights(float a, float b, float c, float d, uint32_t& p0, uint32_t& p1,
+                                              uint32_t& p2) {
+    uint32_t x = pack_f16x2(a, b), y = pack_f16x2(c, d);
+    auto upper = [](uint32_t v) { return v & 0xff00ff00u; };
+    auto rest = [&](uint32_t v) {
+        const uint32_t u = upper(v);
+        const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&u));
+        return *reinterpret_cast<const uint32_t*>(&r);
+    };
+    p0 = __byte_perm(x, y, 0x7531);
+    x = rest(x);
+    y = rest(y);
+    p1 = __byte_perm(x, y, 0x7531);
+    x = rest(x) + 0x00800080u;
+    y = rest(y) + 0x00800080u;
+    p2 = __byte_perm(x, y, 0x7531);
 }
-// Four non-negative weights -> the codes of their high and low parts: 11 bits
-// to f16, 4 of them to e4m3, the exact rest to e4m3 again.
-__device__ __forceinline__ void split_weights(float a, float b, float c, float d, uint32_t& hi,
-                                              uint32_t& lo) {
-    const uint32_t p = pack_f16x2(a, b), q = pack_f16x2(c, d);
-    hi = f16x4_to_e4m3(p, q);
-    uint32_t x, y;
-    e4m3x4_to_f16(hi, x, y);
-    const __half2 r0 = __hsub2(*reinterpret_cast<const __half2*>(&p), *reinterpret_cast<const __half2*>(&x));
-    const __half2 r1 = __hsub2(*reinterpret_cast<const __half2*>(&q), *reinterpret_cast<const __half2*>(&y));
-    lo = f16x4_to_e4m3(*reinterpret_cast<const uint32_t*>(&r0), *reinterpret_cast<const uint32_t*>(&r1));
+
+// 8 consecutive 32-bit columns of this thread's TMEM lane <- r.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 // Waits for a barrier's phase. A wait that runs out makes the tile give up:
@@ -545,10 +558,10 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                     const uint32_t p = tmem_base + kColS + slot * 128 + c * 64;
                     const uint64_t vd = vd0 + (uint32_t)(vs * (kStageBytes >> 4) + c * (kUnitBytes >> 4));
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
+                    for (int part = 0; part < kParts; ++part)
 #pragma unroll
                         for (int kt = 0; kt < kUnit / 32; ++kt)
-                            tc_mma_f8_tmem_a(o_col, p + part * 16 + kt * 8, vd + kt * (4096 >> 4), kIdescPV,
+                            tc_mma_f8_tmem_a(o_col, p + kt * 8 * kParts + part * 8, vd + kt * (4096 >> 4), kIdescPV,
                                              (j | c | part | kt) != 0 ? 1u : 0u);
                     if (c == 0) tc_commit(&obar[slot]);
                 }
@@ -628,6 +641,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
 #pragma unroll
                 for (int e = 0; e < 32; ++e) none[e] = 0u;
                 tmem_st32(scol, none);
+                tmem_st16(scol + 32, reinterpret_cast<const uint32_t(&)[16]>(none));
             } else {
             tile_wait(&sfull[slot], turn & 1, s_abort);
             tc_fence_after();
@@ -740,30 +754,37 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                 __syncwarp();
             }
             if (lane == 0) mbar_arrive(my_dec);
-            uint32_t pk[32];  // 16 words of high parts, 16 of low parts
-            if (mine) {
-                const float add = lv + kShift - m;
-                const float2 mul2 = make_float2(mul, mul), add2 = make_float2(add, add);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float add = lv + kShift - m;
+            const float2 mul2 = make_float2(mul, mul), add2 = make_float2(add, add);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float2 p[2];
+            for (int h = 0; h < 2; ++h) {  // 32 tokens at a time: 8 words of each part
+                uint32_t pk[16], pl[8];
+                if (mine) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float2 x = ffma2(make_float2(__uint_as_float(sv[4 * e + 2 * k]),
-                                                           __uint_as_float(sv[4 * e + 2 * k + 1])), mul2, add2);
-                        p[k] = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                        sum[k] = fadd2(sum[k], p[k]);
+                    for (int e = 0; e < 8; ++e) {
+                        float2 p[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int t = 32 * h + 4 * e + 2 * k;
+                            const float2 x = ffma2(make_float2(__uint_as_float(sv[t]), __uint_as_float(sv[t + 1])), mul2, add2);
+                            p[k] = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+                            sum[k] = fadd2(sum[k], p[k]);
+                        }
+                        split_weights(p[0].x, p[0].y, p[1].x, p[1].y, pk[e], pk[8 + e], pl[e]);
                     }
-                    split_weights(p[0].x, p[0].y, p[1].x, p[1].y, pk[e], pk[16 + e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) pk[e] = pk[8 + e] = pl[e] = 0u;
                 }
+                __syncwarp();
+                tmem_st16(scol + 8 * kParts * h, pk);
+                tmem_st8(scol + 8 * kParts * h + 16, pl);
+            }
+            if (mine) {
                 const float2 t = fadd2(sum[0], sum[1]);
                 l = fmaf(t.x + t.y, fast_exp2(-lv), l);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) pk[e] = 0u;
             }
-            tmem_st32(scol, pk);
             if (any_moves && __any_sync(0xffffffffu, corr != 1.f)) {
                 // O holds earlier units of these rows: rescale once the previous
                 // unit's P V has landed

@@ -119,6 +119,38 @@ def out_tolerance(ref, sizes, dtype, hd, p_bits=24):
     return (rel * vmax)[..., None] + own * ref.abs() + 1e-30
 
 
+def weight_floor(q, k, v, ks, vs, table, bs, ids, ctx_len, q_start):
+    """Per row, head and channel: the row's largest weight * v scale, times the sum
+    of the attended codes' magnitudes. What weights that are off by no less than a
+    fraction of the largest one can add up to, without that fraction."""
+    B, S, Hq, hd = q.shape
+    G = Hq // k.shape[1]
+    out = torch.zeros(B, S, Hq, hd, dtype=torch.float64)
+    for b in range(B):
+        for s in range(S):
+            hi = min(int(q_start[b]) + s, int(ctx_len[b]) - 1)
+            tok = torch.cat([torch.arange(j * bs, max(j * bs, min((j + 1) * bs, hi + 1))) for j in ids[b, s].tolist() if j >= 0])
+            page, off = table[b, tok // bs].long(), tok % bs
+            for h in range(Hq):
+                g = h // G
+                z = (k[page, g, off].double() * ks[page, g].double()[:, None]) @ q[b, s, h].double() / math.sqrt(hd)
+                out[b, s, h] = (torch.softmax(z, 0) * vs[page, g].double()).max() * v[page, g, off].double().abs().sum(0)
+    return out
+
+
+def share_tolerance(ref, share, floor, sizes, dtype, hd, p_bits):
+    """Like out_tolerance, but relative: ``share`` is attend's output over |v|, the
+    sum of weight * |v| of each channel, so that no token's error is measured by
+    another token's larger value. A weight (times its v scale) keeps p_bits bits,
+    half a step of 2^-p_bits of it, or is off by 2^-25 of the row's largest: what a
+    channel sums is off by that much of the sum of its magnitudes, or of
+    ``floor`` (weight_floor's)."""
+    logit = (hd + 16) * 2.0 ** -24 * (sizes[0] + 1.0)
+    rel = 2 * logit + 2.0 ** -p_bits + 2.0 ** -20
+    own = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
+    return rel[..., None] * share + 2.0 ** -25 * floor + own * ref.abs() + 1e-30
+
+
 def lse_tolerance(ref, sizes, hd):
     logit = (hd + 16) * 2.0 ** -24 * (sizes[0] + 1.0)
     return 1.5 * logit + 2.0 ** -20 + 2.0 ** -22 * ref.abs()

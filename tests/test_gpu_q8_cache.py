@@ -1,6 +1,8 @@
 """The 8-bit paged cache on the GPU, against a plain 64-bit reference: the
 append, the attention over it in every schedule, the accumulated block weights
 and the eviction, and a run of them together."""
+import math
+
 import pytest
 import torch
 
@@ -691,3 +693,66 @@ def test_tiles_that_give_up_leave_zeros():
         lci.set_wait_limit_ns(default)
     assert all(torch.equal(a, b) for a, b in zip(call(), want))
     lci.get_device_status()
+
+
+def check_shares(q, k, v, ks, vs, table, bs, ids, ctx, phase):
+    """Output of each channel against what the channel's own tokens add up to."""
+    cache = lci.Q8Cache.wrap(*(t.cuda() for t in (k, v, ks, vs)))
+    bt = lci.create_block_table(table.cuda(), cache.k)
+    S, hd = q.shape[1], q.shape[3]
+    out = lci.sparse_attn_q8(q.cuda(), cache, bt, ids.cuda(), ctx.cuda(), (ctx - S).cuda(), phase=phase)
+    torch.cuda.synchronize()
+    lci.get_device_status()
+    ro, _, _, sizes = ref.attend(q, k.float(), v.float(), ks, vs, table, bs, ids, ctx, ctx - S)
+    share = ref.attend(q, k.float(), v.float().abs(), ks, vs, table, bs, ids, ctx, ctx - S)[0]
+    floor = ref.weight_floor(q, k.float(), v.float(), ks, vs, table, bs, ids, ctx, ctx - S)
+    off = (out.cpu().double() - ro).abs()
+    assert (off <= ref.out_tolerance(ro, sizes, q.dtype, hd, 8 if phase == "prefill" else 11)).all()
+    off = off / ref.share_tolerance(ro, share, floor, sizes, q.dtype, hd, 8 if phase == "prefill" else 11)
+    assert off.max() <= 1, f"{off.max():.2f} of its tolerance"
+
+
+@pytest.mark.parametrize("phase", ["prefill", "decode"])
+@pytest.mark.parametrize("sink", [0.5, 0.7, 0.9, 0.99])
+@pytest.mark.parametrize("nblk,bs", [(32, 64), (128, 64), (256, 64), (256, 128)])
+def test_a_sink_leaves_the_other_tokens_their_share(nblk, bs, sink, phase):
+    """One token takes most of the softmax and has no value: the many small
+    weights behind it are the whole output."""
+    g = torch.Generator().manual_seed(140)
+    S, G, hd, n = 2, 4, 128, nblk * bs
+    q = torch.randn(1, S, G, hd, generator=g)
+    q[..., 0] = 8.0
+    q = q.to(torch.bfloat16)
+    k = torch.randn(nblk, 1, bs, hd, generator=g) * 0.5   # scores of about half a nat
+    v = torch.randn(nblk, 1, bs, hd, generator=g) * 0.5 + 0.5
+    k[..., 0] = 0.0
+    table = torch.randperm(nblk, generator=g).to(torch.int32)[None].contiguous()
+    page = int(table[0, 0])
+    k[page, 0, 0], v[page, 0, 0] = 0.0, 0.0
+    k[page, 0, 0, 0] = (math.log(sink / (1 - sink) * n) + 0.125) * math.sqrt(hd) / 8.0
+    ks = torch.full((nblk, 1), 2.0 ** -4)
+    vs = torch.full((nblk, 1), 2.0 ** -6)
+    k, v = ((x / s[:, :, None, None]).clamp(-448, 448).to(E4M3) for x, s in ((k, ks), (v, vs)))
+    ids = torch.stack([torch.randperm(nblk, generator=g) for _ in range(S)])[None].to(torch.int32)
+    check_shares(q, k, v, ks, vs, table, bs, ids, torch.tensor([n], dtype=torch.int32), phase)
+
+
+@pytest.mark.parametrize("phase", ["prefill", "decode"])
+@pytest.mark.parametrize("apart", [8, 12, 14, 17, 20])
+def test_pages_whose_v_scales_are_far_apart(apart, phase):
+    """Every fourth page's v scale is 2^apart of the others', and its values are in
+    channels of their own: the other channels are the small pages' alone."""
+    g = torch.Generator().manual_seed(141)
+    S, G, hd, bs, nblk = 5, 8, 128, 64, 12
+    q = torch.randn(1, S, G, hd, generator=g).to(torch.bfloat16)
+    k = torch.randn(nblk, 1, bs, hd, generator=g)
+    v = torch.randn(nblk, 1, bs, hd, generator=g) * 100
+    table = torch.randperm(nblk, generator=g).to(torch.int32)[None].contiguous()
+    big = torch.arange(nblk) % 4 == 1
+    v[big, :, :, 64:] = 0.0
+    v[~big, :, :, :64] = 0.0
+    ks = torch.full((nblk, 1), 2.0 ** -6)
+    vs = torch.where(big, 2.0 ** apart, 1.0)[:, None] * 1.25
+    k, v = (k * 64).clamp(-448, 448).to(E4M3), v.clamp(-448, 448).to(E4M3)
+    ids = torch.stack([torch.randperm(nblk, generator=g) for _ in range(S)])[None].to(torch.int32)
+    check_shares(q, k, v, ks, vs, table, bs, ids, torch.tensor([nblk * bs], dtype=torch.int32), phase)
