@@ -667,18 +667,17 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                         }
                         const float big = fmaxf(fmaxf(fmaxf(pa[0], pa[1]), fmaxf(pa[2], pa[3])),
                                                 -fminf(fminf(pi[0], pi[1]), fminf(pi[2], pi[3]))) * fabsf(um);
-                        // cap2 * tanh(S * um) = S * (A + v * (B0 + v * (B1 + ...))), v = S^2, as long
-                        // as every |u| of the warp is small; on packed pairs
-                        const float A = um * cap2, um2 = um * um;
-                        const float2 z2 = make_float2(0.f, 0.f), A2 = make_float2(A, A);
+                        // cap2 * tanh(u), u = S * um, as u * (cap2 + v * (cap2 T0 + v * (cap2 T1 + ...))),
+                        // v = u^2, as long as every |u| of the warp is small; on packed pairs. In u,
+                        // where every term is in range: powers of um alone would underflow.
+                        const float2 z2 = make_float2(0.f, 0.f), um2 = make_float2(um, um), A2 = make_float2(cap2, cap2);
                         if (!__any_sync(0xffffffffu, mine && !(big <= kTanhTiny))) {
-                            const float b0 = A * um2, b1 = b0 * um2, b2 = b1 * um2;
-                            const float2 B0 = make_float2(b0 * kTanhT0, b0 * kTanhT0);
-                            const float2 B1 = make_float2(b1 * kTanhT1, b1 * kTanhT1);
-                            const float2 B2 = make_float2(b2 * kTanhT2, b2 * kTanhT2);
+                            const float2 B0 = make_float2(cap2 * kTanhT0, cap2 * kTanhT0);
+                            const float2 B1 = make_float2(cap2 * kTanhT1, cap2 * kTanhT1);
+                            const float2 B2 = make_float2(cap2 * kTanhT2, cap2 * kTanhT2);
 #pragma unroll
                             for (int e = 0; e < 64; e += 2) {
-                                const float2 x = make_float2(xs[e], xs[e + 1]);
+                                const float2 x = ffma2(make_float2(xs[e], xs[e + 1]), um2, z2);
                                 const float2 v = ffma2(x, x, z2);
                                 const float2 t = ffma2(v, ffma2(v, ffma2(v, B2, B1), B0), A2);
                                 const float2 y = ffma2(x, t, z2);
@@ -686,15 +685,14 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                                 xs[e + 1] = y.y;
                             }
                         } else if (!__any_sync(0xffffffffu, mine && !(big <= kTanhSmall))) {
-                            const float b0 = A * um2, b1 = b0 * um2, b2 = b1 * um2, b3 = b2 * um2, b4 = b3 * um2;
-                            const float2 B0 = make_float2(b0 * kTanhC0, b0 * kTanhC0);
-                            const float2 B1 = make_float2(b1 * kTanhC1, b1 * kTanhC1);
-                            const float2 B2 = make_float2(b2 * kTanhC2, b2 * kTanhC2);
-                            const float2 B3 = make_float2(b3 * kTanhC3, b3 * kTanhC3);
-                            const float2 B4 = make_float2(b4 * kTanhC4, b4 * kTanhC4);
+                            const float2 B0 = make_float2(cap2 * kTanhC0, cap2 * kTanhC0);
+                            const float2 B1 = make_float2(cap2 * kTanhC1, cap2 * kTanhC1);
+                            const float2 B2 = make_float2(cap2 * kTanhC2, cap2 * kTanhC2);
+                            const float2 B3 = make_float2(cap2 * kTanhC3, cap2 * kTanhC3);
+                            const float2 B4 = make_float2(cap2 * kTanhC4, cap2 * kTanhC4);
 #pragma unroll
                             for (int e = 0; e < 64; e += 2) {
-                                const float2 x = make_float2(xs[e], xs[e + 1]);
+                                const float2 x = ffma2(make_float2(xs[e], xs[e + 1]), um2, z2);
                                 const float2 v = ffma2(x, x, z2);
                                 float2 t = ffma2(v, ffma2(v, B4, B3), B2);
                                 t = ffma2(v, ffma2(v, ffma2(v, t, B1), B0), A2);

@@ -756,3 +756,35 @@ def test_pages_whose_v_scales_are_far_apart(apart, phase):
     k, v = (k * 64).clamp(-448, 448).to(E4M3), v.clamp(-448, 448).to(E4M3)
     ids = torch.stack([torch.randperm(nblk, generator=g) for _ in range(S)])[None].to(torch.int32)
     check_shares(q, k, v, ks, vs, table, bs, ids, torch.tensor([nblk * bs], dtype=torch.int32), phase)
+
+
+def capped_inputs(seed, S=40, G=8, ctx=700, bs=64, hd=128):
+    """Keys along the queries, with codes up to the largest: raw products of 2^19 and more."""
+    g = torch.Generator().manual_seed(seed)
+    base = torch.randn(hd, generator=g)
+    q = (base * (1 + 0.05 * torch.randn(1, S, G, hd, generator=g))).to(torch.bfloat16)
+    cache, table, cpu = filled_cache(1, 1, bs, hd, [ctx], seed + 1)
+    k, v, ks, vs = cpu
+    along = 2 * torch.rand(k.shape[:3], generator=g) - 1
+    x = (along[..., None] * base * (1 + 0.05 * torch.randn(k.shape, generator=g)))
+    codes = (x / x.abs().max() * 448).clamp(-448, 448).to(E4M3)
+    raw = k.view(torch.uint8)
+    raw.copy_(torch.where(raw == 0x7F, raw, codes.view(torch.uint8)))  # NaN stays behind the context
+    ks.fill_(2.0 ** -7)
+    ids = torch.stack([torch.randperm(table.shape[1], generator=g) for _ in range(S)])[None].to(torch.int32)
+    ctx_len = torch.tensor([ctx], dtype=torch.int32)
+    p = (ctx_len - S)[:, None] + torch.arange(S, dtype=torch.int32)[None]
+    # the largest attended product, so that a softmax scale sets the largest |z| / cap
+    keys = (k.float().nan_to_num(0.0) * ks[:, :, None, None])[table[0].long()].permute(1, 0, 2, 3).reshape(-1, hd)[:ctx]
+    top = float((q.float().reshape(-1, hd) @ keys.T).abs().max())
+    return lci.Q8Cache.wrap(*(t.cuda() for t in (k, v, ks, vs))), q, table, cpu, bs, ids, ctx_len, ctx_len - S, top
+
+
+@pytest.mark.parametrize("phase", ["prefill", "decode"])
+@pytest.mark.parametrize("u", [0.2, 0.4, 0.6, 2.0])
+@pytest.mark.parametrize("cap", [20.0, 30.0, 50.0, 1000.0])
+def test_caps_over_the_range_of_the_hyperbolic_tangent(cap, u, phase):
+    """Scores up to u times the cap, for each way that tanh is computed."""
+    cache, q, table, cpu, bs, ids, ctx_len, q_start, top = capped_inputs(150)
+    check_attention(q, cache, table, cpu, bs, ids, ctx_len, q_start, phase=phase, mass=phase != "prefill",
+                    p_bits=8 if phase == "prefill" else 11, cap=cap, scale=u * cap / top)
