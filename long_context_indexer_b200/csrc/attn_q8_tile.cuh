@@ -650,6 +650,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
             uint32_t sv[64];
             {
                 tmem_ld64(scol, sv);
+                const bool partial = __any_sync(0xffffffffu, mine && hi - lo != kUnit - 1);
                 if constexpr (MODS) {
                     // raw S -> capped, biased logits in log2 units; then mul = 1
                     float xs[64];
@@ -657,6 +658,11 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                     for (int e = 0; e < 64; ++e) xs[e] = __uint_as_float(sv[e]);
                     if (a.cap > 0.f) {
                         const float um = mul * inv_cap;
+                        // what masked tokens hold has no say in how tanh is computed
+                        if (partial) {
+#pragma unroll
+                            for (int e = 0; e < 64; ++e) xs[e] = e >= lo && e <= hi ? xs[e] : 0.f;
+                        }
                         float pa[4], pi[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) pa[k] = pi[k] = xs[k];
@@ -718,7 +724,7 @@ __global__ void __launch_bounds__(q8t::kThreads, 1) sparse_attn_q8_tile_kernel(
                     for (int e = 0; e < 64; ++e) sv[e] = __float_as_uint(xs[e]);
                     mul = 1.f;
                 }
-                if (__any_sync(0xffffffffu, mine && hi - lo != kUnit - 1)) {
+                if (partial) {
 #pragma unroll
                     for (int e = 0; e < 64; ++e)
                         sv[e] = e >= lo && e <= hi ? sv[e] : __float_as_uint(-INFINITY);

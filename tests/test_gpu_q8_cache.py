@@ -788,3 +788,35 @@ def test_caps_over_the_range_of_the_hyperbolic_tangent(cap, u, phase):
     cache, q, table, cpu, bs, ids, ctx_len, q_start, top = capped_inputs(150)
     check_attention(q, cache, table, cpu, bs, ids, ctx_len, q_start, phase=phase, mass=phase != "prefill",
                     p_bits=8 if phase == "prefill" else 11, cap=cap, scale=u * cap / top)
+
+
+@pytest.mark.parametrize("phase", ["prefill", "decode"])
+@pytest.mark.parametrize("u", [0.2, 0.55])
+def test_slots_that_are_not_attended_change_no_bit(u, phase):
+    """What lies behind the context, and tokens outside a query's window: NaN, zero
+    and the largest codes of either sign give the same bits, under a cap too."""
+    cache, q, table, cpu, bs, ids, ctx_len, q_start, top = capped_inputs(160, S=12, ctx=460)
+    S, n, cap = q.shape[1], int(ctx_len[0]), 30.0
+    p = int(q_start[0]) + torch.arange(S, dtype=torch.int32)
+    first = torch.full((1, S), 70, dtype=torch.int32)   # tokens 0 .. 69 are behind every window
+    last = torch.minimum(p, torch.tensor(400)).to(torch.int32)[None]
+    bt = lci.create_block_table(table.cuda(), cache.k)
+    hide = torch.ones(table.shape[1] * bs, dtype=torch.bool)
+    hide[70:401] = False
+    seen = []
+    along = torch.where(q[0, 0, 0] > 0, 0x7E, 0xFE).to(torch.uint8).cuda()  # +-448 along the queries
+    for code in (0x00, 0x7F, along, along ^ 0x80):  # 0, NaN, the largest products of either sign
+        for pool in (cache.k, cache.v):
+            raw = pool.view(torch.uint8)
+            for j in range(table.shape[1]):
+                raw[int(table[0, j])][:, hide[j * bs:(j + 1) * bs].cuda()] = code
+        got = lci.sparse_attn_q8(q.cuda(), cache, bt, ids.cuda(), ctx_len.cuda(), q_start.cuda(), phase=phase, lse=True,
+                                 cap=cap, scale=u * cap / top, first=first.cuda(), last=last.cuda())
+        torch.cuda.synchronize()
+        lci.get_device_status()
+        seen.append([t.clone() for t in got])
+    # NaN codes of V inside the context make the tile schedule compute rows again: those are as exact, not the same bits
+    alike = seen if phase == "decode" else [seen[0], seen[2], seen[3]]
+    for other in alike[1:]:
+        assert torch.equal(other[0], alike[0][0]) and torch.equal(other[1], alike[0][1])
+    assert torch.isfinite(seen[1][0]).all()
