@@ -443,7 +443,8 @@ LCI_API lci_status lci_sparse_attn_q8(const void* q, lci_dtype dtype, int32_t ba
  *   d_weight[b][j] = decay * d_weight[b][j]
  *                    + sum over s, i with d_ids[b][s][i] == j, and over g, of
  *                      d_mass[b][s][g][i]
- *   d_ids    [batch][S][topk] int32, -1 padded, a row's ids distinct
+ *   d_ids    [batch][S][topk] int32, -1 padded; an id that a row repeats counts
+ *            each time
  *   d_mass   [batch][S][num_kv_heads][topk] float (lci_sparse_attn_q8's)
  *   d_weight [batch][max_blocks] float (updated in place)
  *   decay    finite and >= 0 (1: a plain sum; below 1 the past fades)

@@ -19,7 +19,7 @@ constexpr int kOwn = kRange / (kMinWarps * 32);  // blocks a thread finishes
 constexpr int kAheadMany = 8;
 // the cluster's sums of this CTA's share of the blocks, and a sum per warp and block
 constexpr int kRecv = kRange + kMaxSplit;
-constexpr size_t smem_bytes(int warps) { return (size_t)warps * kRange * 4 + kRecv * 8; }
+constexpr size_t smem_bytes(int warps) { return (size_t)warps * kRange * (4 + 1) + kRecv * 8; }
 }  // namespace bwu
 
 // weight[b][j] = decay * weight[b][j] + sum over s, i with ids[b][s][i] == j of
@@ -27,12 +27,13 @@ constexpr size_t smem_bytes(int warps) { return (size_t)warps * kRange * 4 + kRe
 //
 // Every sum runs in a fixed order without atomics, so results repeat bit for
 // bit: a warp adds its rows one after the other into its own row of kRange
-// fp32 sums in shared memory (the ids of one row are distinct, so its 32 lanes
-// never meet), the CTA adds its warps' sums in 64 bits and stores each into the
+// fp32 sums in shared memory (where lanes hold the same id, they add in their
+// order), the CTA adds its warps' sums in 64 bits and stores each into the
 // CTA of the cluster that finishes the block (distributed shared memory), which
 // adds the CTAs' to the weight. A sequence of more than kRange blocks is cut into
 // ranges, each with its own cluster that reads every entry and keeps those of its
-// range. Bound by latency: an 8K prompt's 2.1 MB (0.3 us of HBM) in 8.7 us, a
+// range. Bound by latency: an 8K prompt's 2.1 MB (0.3 us of HBM) in 10.3 us (1.6 of
+// them the test for repeats; a match over the warp for each item took 15), a
 // serving step of 32 sequences in 2.3. A warp's loads do not wait for one another:
 // with loads behind a test per row and KV head, 64 rows of 64 entries on 8 heads
 // took 42 us against 6.9.
@@ -52,6 +53,7 @@ __global__ void __launch_bounds__((kAhead == 1 ? bwu::kMinWarps : bwu::kMaxWarps
     const int j0 = blockIdx.y * kRange;
     const int width = min(kRange, nb_max - j0);
     float* mine = hist + warp * kRange;
+    volatile uint8_t* owner = reinterpret_cast<uint8_t*>(hist + nw * kRange) + warp * kRange;
     // the blocks that this CTA finishes; their weights are loaded together, ahead
     // of everything else where registers allow it
     const int share = (width + nsplit - 1) / nsplit;
@@ -114,14 +116,37 @@ __global__ void __launch_bounds__((kAhead == 1 ? bwu::kMinWarps : bwu::kMaxWarps
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) add[k] += x[k];
         }
+        // Lanes that hold the same id of a row would meet: each leaves its number with
+        // the block, and one of them finds another's.
+        unsigned other = 0u;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            const unsigned at_j = (unsigned)(id[k] - j0);
-            if (at_j < (unsigned)width)
-                mine[at_j] += add[k];
-            else if ((unsigned)id[k] + 1u > (unsigned)nb_max)
-                raise_status(kStatusBadBlockId);
+            const unsigned at_j = (unsigned)id[k] - (unsigned)j0;
+            const bool on = at_j < (unsigned)width;
+            if (on) owner[at_j] = (uint8_t)lane;
             __syncwarp();
+            other |= on ? owner[at_j] ^ (unsigned)lane : 0u;
+            __syncwarp();
+        }
+        const bool again = __any_sync(0xffffffffu, other != 0u);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const unsigned at_j = (unsigned)id[k] - (unsigned)j0;
+            if (at_j < (unsigned)width) {
+                if (!again) mine[at_j] += add[k];
+            } else if ((unsigned)id[k] + 1u > (unsigned)nb_max) {
+                raise_status(kStatusBadBlockId);
+            }
+            __syncwarp();
+        }
+        if (again) {  // one entry after the other
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                for (int x = 0; x < 32; ++x) {
+                    const unsigned at_j = (unsigned)id[k] - (unsigned)j0;
+                    if (x == lane && at_j < (unsigned)width) mine[at_j] += add[k];
+                    __syncwarp();
+                }
         }
     }
     if constexpr (kAhead > 1) load_weights();

@@ -820,3 +820,23 @@ def test_slots_that_are_not_attended_change_no_bit(u, phase):
     for other in alike[1:]:
         assert torch.equal(other[0], alike[0][0]) and torch.equal(other[1], alike[0][1])
     assert torch.isfinite(seen[1][0]).all()
+
+
+@pytest.mark.parametrize("S,topk,NB", [(1, 32, 3), (1, 5, 1), (40, 70, 8), (700, 33, 1100), (3, 256, 40)])
+def test_block_weights_add_every_repeat_of_an_id(S, topk, NB):
+    """Rows that hold a block more than once: each entry counts, and a repeat of the call gives the same bits."""
+    g = torch.Generator().manual_seed(8)
+    H = 2
+    ids = torch.randint(-1, NB, (2, S, topk), generator=g).to(torch.int32)
+    ids[0, 0] = NB - 1  # one block everywhere
+    mass = torch.rand(2, S, H, topk, generator=g)
+    weight = torch.rand(2, NB, generator=g)
+    got = lci.block_weight_update(weight.cuda(), ids.cuda(), mass.cuda(), decay=0.5)
+    torch.cuda.synchronize()
+    lci.get_device_status()
+    want = ref.weight_update(weight, ids, mass, 0.5)
+    # fp32 sums of at most n addends of H masses each, one rounding of the total
+    n = max(int(torch.bincount(ids[b][ids[b] >= 0].long().flatten()).max()) for b in range(2))
+    assert ((got.cpu().double() - want).abs() <= want * 2.0 ** -24 * (H + 2 + n) + 1e-30).all()
+    for _ in range(5):
+        assert torch.equal(got, lci.block_weight_update(weight.cuda(), ids.cuda(), mass.cuda(), decay=0.5))
