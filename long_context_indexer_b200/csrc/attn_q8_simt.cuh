@@ -42,7 +42,8 @@ struct AttnQ8Args {
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
-// v scales below this count as this (the softmax weight carries log2 of it)
+// v scales below this count as this (in the tensor-core schedules the softmax weight
+// carries log2 of it)
 constexpr float kMinVScale = 8.673617379884035e-19f;  // 2^-60
 
 // First and last token a query row may attend; an empty range has hi < lo.
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(kQ8SimtWarps * 32) sparse_attn_q8_simt_kernel(
                 const size_t cell = (size_t)page * a.H_kv + g;
                 const uint8_t* kb = a.k + cell * bs * hd;
                 const uint8_t* vb = a.v + cell * bs * hd;
-                const float kmul = a.scale * a.ks[cell], vmul = a.vs[cell];
+                const float kmul = a.scale * a.ks[cell], vmul = fmaxf(a.vs[cell], kMinVScale);
                 for (int u0 = 0; u0 < bs; u0 += 32) {
                     const int u = u0 + lane, t = j * bs + u;
                     const bool see = u < bs && t >= win.lo && t <= win.hi;

@@ -195,7 +195,7 @@ __device__ __noinline__ void q8_row_by_warp(const AttnQ8Args& a, int row, int h,
         const int page = q8_page(a, b, j, win);
         if (page < 0) continue;
         const size_t cell = (size_t)page * a.H_kv + g;
-        const float kmul = a.scale * a.ks[cell], vmul = a.vs[cell];
+        const float kmul = a.scale * a.ks[cell], vmul = fmaxf(a.vs[cell], kMinVScale);
         for (int u0 = 0; u0 < a.bs; u0 += 32) {
             const int t = j * a.bs + u0 + lane;
             const bool see = u0 + lane < a.bs && t >= win.lo && t <= win.hi;

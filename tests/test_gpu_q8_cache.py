@@ -840,3 +840,25 @@ def test_block_weights_add_every_repeat_of_an_id(S, topk, NB):
     assert ((got.cpu().double() - want).abs() <= want * 2.0 ** -24 * (H + 2 + n) + 1e-30).all()
     for _ in range(5):
         assert torch.equal(got, lci.block_weight_update(weight.cuda(), ids.cuda(), mass.cuda(), decay=0.5))
+
+
+@pytest.mark.parametrize("shape,phase", [(SHAPES[5], "prefill"), (SHAPES[5], "decode"), (SHAPES[10], "auto")])
+def test_v_scales_below_the_floor_count_as_the_floor(shape, phase):
+    """In every schedule, and in rows that the tile schedule computes again (here
+    for a NaN in another channel)."""
+    q, cache, table, cpu, bs, ids, ctx_len, q_start = attention_inputs(shape, 170)
+    k, v, ks, vs = cpu
+    vs.fill_(2.0 ** -70)
+    floor = torch.full_like(vs, 2.0 ** -60)
+    clean = v.clone()
+    v.view(torch.uint8)[int(table[0, 0]), 0, 0, 3] = 0x7F
+    cache = lci.Q8Cache.wrap(*(t.cuda() for t in (k, v, ks, vs)))
+    bt = lci.create_block_table(table.cuda(), cache.k)
+    out = lci.sparse_attn_q8(q.cuda(), cache, bt, ids.cuda(), ctx_len.cuda(), q_start.cuda(), phase=phase).cpu().double()
+    lci.get_device_status()
+    ro, _, _, sizes = ref.attend(q, k.float(), clean.float(), ks, floor, table, bs, ids, ctx_len, q_start)
+    # in units of the floor: 1e-30 of out_tolerance is far above these values
+    tol = ref.out_tolerance(ro * 2.0 ** 60, (sizes[0], sizes[1] * 2.0 ** 60), q.dtype, q.shape[3],
+                            24 if q.dtype == torch.float32 else 8) * 2.0 ** -60
+    keep = torch.arange(q.shape[3]) != 3
+    assert ((out - ro).abs() <= tol)[..., keep].all()
