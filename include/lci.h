@@ -405,7 +405,8 @@ typedef struct {
  *   d_mass   [batch][S][num_kv_heads][topk] float or NULL (output): the softmax
  *            weight that the tokens of block d_ids[b][s][i] received, summed
  *            over the query heads of the KV head; 0 for -1 entries. A row's
- *            entries add up to H_q / num_kv_heads (0 where nothing is attended).
+ *            entries add up to H_q / num_kv_heads (0 where nothing is attended);
+ *            in a row that attends a NaN, every attended block's is NaN
  * A row without an attended token is zero. Rows of d_ids may be in any order,
  * may hold -1 anywhere, and must not repeat a block. Slots that are not
  * attended are never read into a result, whatever they hold; a NaN that is

@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kQ8SimtWarps * 32) sparse_attn_q8_simt_kernel(
         if (a.lse && tid == 0) a.lse[(size_t)row * a.H_q + h] = L == 0.f ? -INFINITY : M + log2f(L);
         if (a.mass)
             for (int i = tid; i < a.topk; i += blockDim.x)
-                bt[i] += bm[i] == -INFINITY ? 0.f : br[i] * exp2f(bm[i] - base) * inv;
+                bt[i] += br[i] == 0.f ? 0.f : br[i] * exp2f(bm[i] - base) * inv;  // a NaN stays one
     }
     if (a.mass) {
         float* mrow = a.mass + ((size_t)row * a.H_kv + g) * a.topk;

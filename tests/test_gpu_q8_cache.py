@@ -862,3 +862,37 @@ def test_v_scales_below_the_floor_count_as_the_floor(shape, phase):
                             24 if q.dtype == torch.float32 else 8) * 2.0 ** -60
     keep = torch.arange(q.shape[3]) != 3
     assert ((out - ro).abs() <= tol)[..., keep].all()
+
+
+@pytest.mark.parametrize("shape", [SHAPES[2], SHAPES[10], (torch.float32, 1, 4, 70, 1, 9, 64, 16, 5)])
+def test_masses_of_rows_that_meet_a_nan(shape):
+    """A NaN among the attended keys makes the mass of every attended block of the
+    row NaN, a block whose only token it is among them; other rows are what they
+    are without it."""
+    q, cache, table, cpu, bs, ids, ctx_len, q_start = attention_inputs(shape, 180)
+    k, v, ks, vs = cpu
+    B, S = q.shape[:2]
+    n = int(ctx_len[0])
+    last = (n - 1) // bs
+    for s in range(S):  # each row: the last block (one NaN in it), a hole, others
+        ids[0, s] = -1
+        ids[0, s, 0], ids[0, s, -1] = last, 0
+    ids[0, 0, 0] = -1  # a row that does not select the block
+    ctx_len[0] = last * bs + 1  # and only one token of it is attended: the NaN
+    q_start[0] = int(ctx_len[0]) - 1
+    clean = k.clone()
+    k.view(torch.uint8)[int(table[0, last]), :, 0, 5] = 0x7F
+    out = []
+    for kk in (k, clean):
+        cache = lci.Q8Cache.wrap(*(t.cuda() for t in (kk, v, ks, vs)))
+        bt = lci.create_block_table(table.cuda(), cache.k)
+        got = lci.sparse_attn_q8(q.cuda(), cache, bt, ids.cuda(), ctx_len.cuda(), q_start.cuda(), phase="decode", lse=True, mass=True)
+        torch.cuda.synchronize()
+        lci.get_device_status()
+        out.append([t.cpu() for t in got])
+    (o, l, m), (o2, l2, m2) = out
+    hit = torch.zeros(B, S, dtype=torch.bool)
+    hit[0, 1:] = True
+    assert o[hit].isnan().all() and l[hit].isnan().all()
+    assert (m2[hit] != 0).any() and m[hit][m2[hit] != 0].isnan().all()
+    assert torch.equal(o[~hit], o2[~hit]) and torch.equal(m[~hit], m2[~hit])
