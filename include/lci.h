@@ -377,7 +377,7 @@ LCI_API lci_status lci_kv_append_q8(const void* k_new, const void* v_new, lci_dt
 /*
  * Changes of the scores before the softmax; zero-initialise, then set what is
  * wanted. With z the scaled logit of query position p and token t:
- *   cap > 0      z becomes cap * tanh(z / cap)
+ *   cap > 0      z becomes cap * tanh(z / cap); within 2^-100 .. 2^100
  *   d_slopes     [H_q] float: slopes[h] * |p - t| is subtracted (after the cap)
  *   d_first      [batch][S] int32: tokens before d_first[b][s] are not attended
  *                (a document mask: the start of the query's document)

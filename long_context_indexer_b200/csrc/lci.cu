@@ -1753,8 +1753,9 @@ lci_status lci_sparse_attn_q8(const void* q, lci_dtype dtype, int32_t batch, int
         return fail(LCI_ERR_INVALID_ARG, "sparse_attn_q8: non-finite scale");
     lci_score_options opt = {};
     if (options) opt = *options;
-    if (!std::isfinite(opt.cap) || opt.cap < 0.f)
-        return fail(LCI_ERR_INVALID_ARG, "sparse_attn_q8: cap must be finite and >= 0");
+    // within a range whose reciprocal and products with log2(e) are normal numbers
+    if (!(opt.cap == 0.f || (opt.cap >= 0x1p-100f && opt.cap <= 0x1p100f)))
+        return fail(LCI_ERR_INVALID_ARG, "sparse_attn_q8: cap must be 0 or within 2^-100 .. 2^100");
     if (topk > lci::kMaxTopk)
         return fail(LCI_ERR_UNSUPPORTED, "sparse_attn_q8: topk %d above %d", topk, lci::kMaxTopk);
     if (table->head_dim % 32 != 0 || table->head_dim > lci::kQ8MaxHd)

@@ -744,7 +744,7 @@ def sparse_attn_q8(q: torch.Tensor, cache: Q8Cache, table: BlockTable, ids: torc
     """A3+A4 over the 8-bit cache: attention of q [B, S, H_q, hd] (bf16 or fp32)
     over the selected blocks ids [B, S, topk].
 
-    cap > 0 caps the scaled scores z at cap * tanh(z / cap); slopes [H_q] fp32
+    cap > 0 (2^-100 .. 2^100) caps the scaled scores z at cap * tanh(z / cap); slopes [H_q] fp32
     subtracts slopes[h] * |p - t|; first / last [B, S] int32 bound the tokens a
     query attends (document mask: first = its document's start; prefix mask:
     last = max(p, prefix - 1)). lse and mass are True or output tensors: the

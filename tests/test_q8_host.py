@@ -249,3 +249,14 @@ def test_calls_prepared_over_a_closed_table_are_refused(lib, monkeypatch):
     with pytest.raises(ValueError, match="closed"):
         step()
     assert len(made) == 2
+
+
+def test_caps_outside_the_range_are_refused(lib, tables):
+    """A cap whose reciprocal is infinite would turn scores of zero into NaN."""
+    class Opt(ctypes.Structure):
+        _fields_ = [("cap", ctypes.c_float), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("c", ctypes.c_void_p)]
+    for cap in (1e-40, 2.0 ** -101, 2.0 ** 101, 3e38, -0.5):
+        opt = Opt(cap, None, None, None)
+        assert lib.lci_sparse_attn_q8(FAKE, 1, 2, 1, 16, FAKE, FAKE, FAKE, FAKE, tables["q8"], FAKE, 4, FAKE, FAKE, 0.0,
+                                      ctypes.byref(opt), 0, FAKE, None, None, None) == INVALID, cap
+        assert b"cap" in lib.lci_last_error()
