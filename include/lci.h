@@ -425,8 +425,8 @@ typedef struct {
  * blocks that a row attends lie within 2^96 of each other.
  * LCI_PHASE_PREFILL asks for the first where it fits, DECODE rules it out, AUTO
  * chooses by an estimate from the sizes. The lengths are on the device, so the
- * estimate takes max_blocks for them: ask for PREFILL where a prompt is much
- * shorter than the table.
+ * estimate weighs a prompt that starts its sequence against a context that fills
+ * the table: ask for PREFILL or DECODE where a program knows better.
  * Limits: H_q a multiple of num_kv_heads, head_dim a multiple of 32 and <= 256,
  * topk <= 256, max_blocks * block_size < 2^31. Needs no workspace.
  */

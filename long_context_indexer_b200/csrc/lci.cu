@@ -1650,13 +1650,19 @@ lci_status launch_tile(const lci::AttnQ8Args& a, int32_t batch, const lci_block_
 }
 
 // Which schedule a call takes: the tile schedule when asked for and it fits, or,
-// left to choose, the one with the lower estimate, in SM cycles. A tile costs
-// about 16 K of set-up and output and 1030 per 64-token unit of its union (1700
-// when scores are capped or biased), a row 2800 and 800 (1000) per unit, the
-// row-wise launch 8 K; the union is that of random selections. Measured, tile
-// against rows: 11 blocks, 888 queries of 4 heads 25 us / 74; 3 blocks, 264 rows
-// 15.7 / 9.9; 116 blocks, 5 of them for each of 1880 rows 38 / 50; 288 blocks, 9 for
-// each of 5838 rows with a cap 304 / 224.
+// left to choose, the one that an estimate prefers, in SM cycles. A tile costs
+// about 16 K of set-up and output and 1000 per 64-token unit of its union (1350
+// when scores are capped or biased), a row 2800 and 800 per unit, the row-wise
+// launch 8 K; the union is that of random selections among nb blocks. The lengths
+// are on the device: nb lies between what the call's queries or picks take up
+// (a prompt from its start) and the table's max_blocks (a late chunk, or a table
+// with room). The tile schedule is chosen where its loss at the upper end, against
+// the rows, is below the rows' loss at the lower end. Measured, tile against rows
+// in us: 8K prompt 298 / 588, in a table 16 times as large the same; 2 x 4096
+// tokens of documents, capped, 153 / 610; 4096 queries of 16 picks among 8192
+// blocks of 128, which share none, 552 / 428; 2 x 2919 of 9 among 288, capped, 263
+// / 200; 4096 of 16 among 1024, capped, 359 / 231; 1880 of 5 among 116 41 / 43;
+// 512 of 32 among 128 72 / 64; 264 of 3 among 5 13 / 7; 64 of 16 among 64 44 / 11.
 bool use_tile_q8(const lci::AttnQ8Args& a, lci_dtype dtype, const lci_block_table* t,
                  int32_t batch, lci_phase phase) {
     if (phase == LCI_PHASE_DECODE || !tile_q8_fits(a, dtype, t)) return false;
@@ -1665,13 +1671,14 @@ bool use_tile_q8(const lci::AttnQ8Args& a, lci_dtype dtype, const lci_block_tabl
     constexpr double kSMs = 148;
     const bool mods = a.cap > 0.f || a.slopes;
     const int QT = tile_q8_queries(a);
-    const double nb = a.nb_max, k = std::min(a.topk, a.nb_max), upb = a.bs / lci::q8t::kUnit;
-    const double queries = std::min(QT, a.S);
-    const double uni = nb * (1.0 - std::pow(1.0 - k / nb, queries));
-    const double tiles = (double)batch * a.H_kv * ((a.S + QT - 1) / QT);
-    const double tile = std::ceil(tiles / kSMs) * (16e3 + uni * upb * (mods ? 1700 : 1030));
-    const double rows = 8e3 + (double)batch * a.H_kv * a.S * (2800 + k * upb * (mods ? 1000 : 800)) / kSMs;
-    return tile < rows;
+    const double k = std::min(a.topk, a.nb_max), upb = a.bs / lci::q8t::kUnit;
+    const double queries = std::min(QT, a.S), waves = std::ceil((double)batch * a.H_kv * ((a.S + QT - 1) / QT) / kSMs);
+    auto tile = [&](double nb) {
+        return waves * (16e3 + nb * (1.0 - std::pow(1.0 - k / nb, queries)) * upb * (mods ? 1350 : 1000));
+    };
+    const double most = a.nb_max, least = std::min(most, std::max(k, std::ceil((double)a.S / a.bs)));
+    const double rows = 8e3 + (double)batch * a.H_kv * a.S * (2800 + k * upb * 800) / kSMs;
+    return tile(most) * tile(least) < rows * rows;
 }
 
 template <int IPT>

@@ -896,3 +896,25 @@ def test_masses_of_rows_that_meet_a_nan(shape):
     assert o[hit].isnan().all() and l[hit].isnan().all()
     assert (m2[hit] != 0).any() and m[hit][m2[hit] != 0].isnan().all()
     assert torch.equal(o[~hit], o2[~hit]) and torch.equal(m[~hit], m2[~hit])
+
+
+@pytest.mark.parametrize("times", [1, 4, 16, 128])
+@pytest.mark.parametrize("S,topk,G,bs,cap", [(2048, 16, 16, 64, 0.0), (2048, 8, 8, 128, 0.0), (3000, 16, 4, 64, 20.0)])
+def test_a_prompt_takes_the_tile_schedule_in_tables_of_any_length(S, topk, G, bs, cap, times):
+    """The schedules round weights differently: equal bits tell which one ran."""
+    g = torch.Generator().manual_seed(190)
+    cache, table, cpu = filled_cache(1, 1, bs, 128, [S], 191)
+    nb = table.shape[1]
+    wide = torch.full((1, min(nb * times, 16384)), -1, dtype=torch.int32)
+    wide[:, :nb] = table
+    q = torch.randn(1, S, G, 128, generator=g).to(torch.bfloat16).cuda()
+    ids = torch.rand(S, nb, generator=g)
+    ids[torch.arange(nb)[None] * bs > torch.arange(S)[:, None]] = -1.0  # blocks behind the query
+    best = ids.topk(topk, dim=1)
+    ids = torch.where(best.values >= 0, best.indices, -1).to(torch.int32)[None].cuda()
+    bt = lci.create_block_table(wide.cuda(), cache.k)
+    ctx, p0 = torch.tensor([S], dtype=torch.int32).cuda(), torch.zeros(1, dtype=torch.int32).cuda()
+    out = {ph: lci.sparse_attn_q8(q, cache, bt, ids, ctx, p0, cap=cap, phase=ph) for ph in ("auto", "prefill", "decode")}
+    torch.cuda.synchronize()
+    lci.get_device_status()
+    assert torch.equal(out["auto"], out["prefill"]) and not torch.equal(out["auto"], out["decode"])
