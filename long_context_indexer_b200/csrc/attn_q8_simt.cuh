@@ -9,7 +9,8 @@
 // online softmax, and for P V the lanes split the head dim. The warps' (max, sum,
 // O) merge through shared memory. Bound by instruction issue: about two
 // conversions and four multiply-adds per four cached elements (32 rows x 16 heads
-// x 32 blocks of 64, fp32: 131 us; with a row's heads in one CTA 1452).
+// x 32 blocks of 64, fp32: 126 us, with masses 208; with a row's heads in one CTA
+// 1452).
 #pragma once
 
 #include <cooperative_groups.h>
@@ -82,17 +83,18 @@ __device__ __forceinline__ int q8_page(const AttnQ8Args& a, int b, int j, const 
     return first <= w.hi && first + a.bs > w.lo ? page : -1;
 }
 
-// tanh(u): below 0.625 the odd polynomial u + u^3 * (c0 + ... + c4 u^8), fitted
-// to tanh(u) / u over u^2 (relative error 5e-9 before rounding); above it
-// 1 - 2 / (2^(2 log2(e) |u|) + 1), whose error of 2^-22 is relative to 1.
+// tanh(u): below 0.625 the odd polynomial u + u^3 * (c0 + ... + c4 u^8), a least
+// squares fit of the relative error at Chebyshev nodes of u^2 (1e-8 at most; the
+// tests hold the fit); above it 1 - 2 / (2^(2 log2(e) |u|) + 1), whose error of
+// 2^-22 is relative to 1.
 constexpr float kTanhSmall = 0.625f;
-constexpr float kTanhC0 = -0.3333328068256378f, kTanhC1 = 0.13331441581249237f,
-                kTanhC2 = -0.05373971164226532f, kTanhC3 = 0.020639076828956604f,
-                kTanhC4 = -0.00570497615262866f;
-// the same with three coefficients for |u| <= 0.25 (relative error 3e-9)
+constexpr float kTanhC0 = -0.3333328068256378f, kTanhC1 = 0.13331381976604462f,
+                kTanhC2 = -0.05373531952500343f, kTanhC3 = 0.020626291632652283f,
+                kTanhC4 = -0.005691985599696636f;
+// the same with three coefficients for |u| <= 0.25 (relative error 4e-9)
 constexpr float kTanhTiny = 0.25f;
-constexpr float kTanhT0 = -0.3333323895931244f, kTanhT1 = 0.13324236869812012f,
-                kTanhT2 = -0.05143002048134804f;
+constexpr float kTanhT0 = -0.3333323895931244f, kTanhT1 = 0.13324128091335297f,
+                kTanhT2 = -0.05141825973987579f;
 __device__ __forceinline__ float q8_tanh_small(float u) {
     const float v = u * u;
     const float p = fmaf(v, fmaf(v, fmaf(v, fmaf(v, kTanhC4, kTanhC3), kTanhC2), kTanhC1), kTanhC0);

@@ -20,8 +20,9 @@
 //   S  = Qhi K^T + Qlo K^T       M=128, N=128 tokens, A = Q from shared memory
 //   O += P0 V + P1 V + P2 V      M=128, N=128 dims, K=64 tokens, A = P from TMEM,
 //                                B = V MN-major from shared memory
-// (Q stays out of TMEM so that three pairs of S fit beside O.) The third part
-// costs 8 % (8K prompt). V converted to f16 for two-byte weights was slower: by
+// (Q stays out of TMEM so that three pairs of S fit beside O.) The third part costs
+// 35 us of the 8K prompt; two parts keep 7 bits, which raises the output's error by
+// two thirds (1.3e-4 -> 2.1e-4, against 1.3e-4 of a bf16 rounding alone). V converted to f16 for two-byte weights was slower: by
 // the softmax warps 351 us, by warps of their own 325 to 429, against 300.
 //
 // Scales. A block's k scale multiplies the fp32 logits. Its v scale enters the
@@ -40,14 +41,15 @@
 // on a row's reference in unit order: a short chain of one mbarrier per 32 rows
 // and group, between the maximum and the exponentials of each unit.
 //
-// Bound. 8K prompt, 16 heads on one KV head, 32 blocks of 64 per query: 284 us, 423
-// TFLOP/s of useful work (25 % of the measured bf16 peak; the selections make the
-// MMAs compute about twice that). About 1000 cycles per unit of a tile's union
-// against 514 of MMA: with three pairs in flight the softmax (1700 cycles for a
-// unit that a warp's queries selected, 64 exponentials a thread and the two
-// roundings of each weight), its hand-over to the MMA and the wait for the slot
-// set the pace, and 16 thousand cycles per tile go to the union, the first copies
-// and the output.
+// Bound. 8K prompt, 16 heads on one KV head, 32 blocks of 64 per query: 299 us a
+// call in a graph, 402 TFLOP/s of useful work (24 % of the measured bf16 peak; the
+// selections make the MMAs compute about twice that), 336 us a call on its own.
+// About 1000 cycles per unit of a tile's union against 640 of MMA (tensor pipe 50 %
+// active): with three pairs in flight the softmax (64 exponentials a thread and the
+// parts of each weight), its hand-over to the MMA and the wait for the slot set the
+// pace, and 16 thousand cycles per tile go to the union, the first copies and the
+// output. More softmax warps do not help (four groups that read S twice, in halves,
+// to fit their registers: 312 us; three groups so: 305).
 //
 // Unset memory and NaN. V rows of absent units and of tokens past the context
 // are zeroed in shared memory before the MMA reads them, their scores masked. A

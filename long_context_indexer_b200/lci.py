@@ -749,7 +749,9 @@ def sparse_attn_q8(q: torch.Tensor, cache: Q8Cache, table: BlockTable, ids: torc
     query attends (document mask: first = its document's start; prefix mask:
     last = max(p, prefix - 1)). lse and mass are True or output tensors: the
     base-2 log-sum-exp [B, S, H_q], and the softmax weight each selected block
-    received [B, S, H_kv, topk], summed over the KV head's query heads.
+    received [B, S, H_kv, topk], summed over the KV head's query heads. phase
+    "prefill" or "decode" picks the schedule where the sizes alone do not tell: a
+    prompt much shorter than the table, a late chunk whose queries share few blocks.
     Returns out, or (out[, lse][, mass]) with those asked for."""
     return prepare_sparse_attn_q8(q, cache, table, ids, ctx_len, q_start, scale, cap, slopes, first,
                                   last, phase, out, lse, mass)(stream)
@@ -779,7 +781,8 @@ def block_weight_update(weight: torch.Tensor, ids: torch.Tensor, mass: torch.Ten
 
 def prepare_cache_evict(table: BlockTable, ctx_len: torch.Tensor, weight: torch.Tensor, budget: int,
                         sink: int = 0, recent: int = 1, in_place: bool = False) -> PreparedCall:
-    """cache_evict as a PreparedCall."""
+    """cache_evict as a PreparedCall; its outputs are tensors of their own unless
+    ``in_place`` is set, so that calling it again gives the same."""
     if weight.dim() != 2:
         raise ValueError("lci: weight must be [B, max_blocks]")
     B, NB = weight.shape

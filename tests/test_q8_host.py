@@ -260,3 +260,43 @@ def test_caps_outside_the_range_are_refused(lib, tables):
         assert lib.lci_sparse_attn_q8(FAKE, 1, 2, 1, 16, FAKE, FAKE, FAKE, FAKE, tables["q8"], FAKE, 4, FAKE, FAKE, 0.0,
                                       ctypes.byref(opt), 0, FAKE, None, None, None) == INVALID, cap
         assert b"cap" in lib.lci_last_error()
+
+
+@pytest.mark.parametrize("names,limit,bound", [("C0 C1 C2 C3 C4", 0.625, 1e-8), ("T0 T1 T2", 0.25, 4e-9)])
+def test_tanh_polynomials_are_the_fit(names, limit, bound):
+    """The coefficients are a least squares fit of the relative error of
+    u + u^3 (c0 + c1 u^2 + ...) at Chebyshev nodes of u^2 in [0, limit^2]."""
+    import os
+    import re
+
+    import numpy as np
+    src = open(os.path.join(os.path.dirname(lci.__file__), "csrc", "attn_q8_simt.cuh")).read()
+    have = np.array([float(re.search(rf"kTanh{n} = (-?[0-9.]+)f", src).group(1)) for n in names.split()])
+    k = np.arange(400)
+    v = limit ** 2 * (0.5 - 0.5 * np.cos((2 * k + 1) * np.pi / 800))
+    u = np.sqrt(v)
+    weight = v * u / np.tanh(u)
+    fit = np.linalg.lstsq(np.vander(v, len(have), increasing=True) * weight[:, None],
+                          (np.tanh(u) / u - 1) / v * weight, rcond=None)[0]
+    assert np.allclose(have, fit, rtol=1e-6, atol=0)
+    u = np.linspace(1e-4, limit, 100001)
+    poly = u + u ** 3 * sum(c * u ** (2 * i) for i, c in enumerate(have))
+    assert np.abs(poly / np.tanh(u) - 1).max() <= bound
+
+
+def test_weight_parts_add_up():
+    """The tile schedule's three 8-bit parts of a weight, for every f16 that a
+    weight can be: within 2^-9 of it, or 2^-17 where it is below 2^-8."""
+    bits = torch.arange(1, int(torch.tensor(2.0 ** 15.75, dtype=torch.float16).view(torch.int16)) + 1, dtype=torch.int32)
+    w = bits.to(torch.int16).view(torch.float16)
+
+    def upper(x):  # the e5m2 number in the upper byte
+        return (x.view(torch.int16) & -256).view(torch.float16)
+    p0 = upper(w)
+    p1 = upper(w - p0)
+    p2 = upper((w - p0 - p1).view(torch.int16).add(0x80).view(torch.float16))
+    for p in (p0, p1, p2):
+        assert torch.equal(p.to(torch.float8_e5m2).to(torch.float16), p)
+    off = (p0.double() + p1.double() + p2.double() - w.double()).abs()
+    large = w >= 2.0 ** -8
+    assert (off[large] <= w.double()[large] * 2.0 ** -9).all() and (off[~large] <= 2.0 ** -17).all()
