@@ -918,3 +918,14 @@ def test_a_prompt_takes_the_tile_schedule_in_tables_of_any_length(S, topk, G, bs
     torch.cuda.synchronize()
     lci.get_device_status()
     assert torch.equal(out["auto"], out["prefill"]) and not torch.equal(out["auto"], out["decode"])
+
+
+@pytest.mark.parametrize("shape,phase", [(SHAPES[5], "prefill"), (SHAPES[5], "decode"), (SHAPES[0], "decode"), (SHAPES[10], "auto")])
+def test_v_scales_at_the_largest_distance(shape, phase):
+    """Blocks whose v scales are 2^96 apart: the softmax itself does not see them."""
+    q, cache, table, cpu, bs, ids, ctx_len, q_start = attention_inputs(shape, 200)
+    k, v, ks, vs = cpu
+    vs.copy_(torch.where(torch.arange(len(vs)) % 2 == 0, 2.0 ** 48, 2.0 ** -48)[:, None].expand_as(vs))
+    cache = lci.Q8Cache.wrap(*(t.cuda() for t in (k, v, ks, vs)))
+    check_attention(q, cache, table, (k, v, ks, vs), bs, ids, ctx_len, q_start, phase=phase, mass=phase != "prefill",
+                    p_bits=8 if phase == "prefill" else 11)
